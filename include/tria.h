@@ -20,6 +20,11 @@
  *   compaction    survivors move in place to slots [0, kept) in ascending slot
  *                 order; seq_len becomes kept.
  *
+ * Around the prune it has the steps of a decode loop over the pruned cache: one
+ * token at a time (tria_append, tria_decode_attention), or a tree of drafted
+ * tokens at a time (tria_tree_attention, tria_tree_commit), with the cache in one
+ * segment per sequence or in pages (tria_pages, tria_block_tables).
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Pointers marked DEVICE must point to memory of the current CUDA device;
@@ -83,6 +88,7 @@ typedef enum {
 #define TRIA_MAX_BATCH 256
 #define TRIA_MAX_OFFSETS 4096
 #define TRIA_MAX_SEGMENT (1 << 18)
+#define TRIA_MAX_NODES 256       /* nodes of a drafted tree */
 
 /* device error word bits */
 #define TRIA_DEVERR_SEQ_LEN 1      /* seq_len[b] < 0 or > segment capacity: that sequence skipped */
@@ -91,6 +97,9 @@ typedef enum {
 #define TRIA_DEVERR_SEGMENT_BIG 8  /* a live sequence exceeded the kernel's per-unit capacity */
 #define TRIA_DEVERR_SEGMENT_FULL 16 /* tria_append: no free slot in a segment: that sequence skipped */
 #define TRIA_DEVERR_BUDGET 32      /* a head budget outside [1, budget]: that KV head's units skipped */
+#define TRIA_DEVERR_TREE 64        /* a tree's node count, parent or accepted node out of range (see tria_tree) */
+#define TRIA_DEVERR_PAGES 128      /* a block id, a held count, the pool's ring or a slot map entry out of range */
+#define TRIA_DEVERR_POOL 256       /* tria_block_tables: the pool has too few free blocks: that sequence skipped */
 
 /* Host-side description of the prune problem, copied by value. */
 typedef struct {
@@ -123,7 +132,23 @@ typedef struct {
                            The prune window applies per unit: head budget + window. */
 } tria_config;
 
-/* The cache.  Device pointers except seq_start. */
+/* A paged cache's bookkeeping (dimensionstp.github.io review, section 6, Limitations: in
+ * serving, the pruned cache meets a paged KV cache).  The slots of a (layer, KV head) row
+ * are n_blocks blocks of block_size; token t of sequence b lives in slot
+ * block_table[b][t / block_size] * block_size + t % block_size, the same one in every row.
+ * tria_block_tables keeps the arrays; a program fills them once: block_table all -1, held
+ * all 0, ring = 0..n_blocks-1 in any order, ring_state = {0, n_blocks}. */
+typedef struct {
+  int32_t *block_table;    /* DEVICE int32 [B][max_blocks]: block ids, -1 past held[b] */
+  int32_t *held;           /* DEVICE int32 [B]: blocks that each sequence holds */
+  int32_t *ring;           /* DEVICE int32 [n_blocks]: the pool, a ring of free block ids */
+  int32_t *ring_state;     /* DEVICE int32 [2]: the ring's head, and how many blocks are free */
+  int32_t block_size;      /* 16, 32, 64, 128 or 256 */
+  int32_t n_blocks;
+  int32_t max_blocks;      /* >= every segment's capacity / block_size, rounded up */
+} tria_pages;
+
+/* The cache.  Device pointers except seq_start and pages. */
 typedef struct {
   void *k;                 /* DEVICE bf16 [L][Hkv][cap_total][D], 16-byte aligned */
   void *v;                 /* DEVICE bf16 [L][Hkv][cap_total][D], 16-byte aligned */
@@ -138,7 +163,27 @@ typedef struct {
                               g)*B + b] slots of its segment (units of one sequence may
                               differ, as after a prune with head budgets); seq_len is then
                               neither read nor written and may be NULL. */
+  const tria_pages *pages; /* HOST, or NULL: sequences in segments.  When set, slots are
+                              found through the block tables, cap_total is n_blocks *
+                              block_size, and seq_start only bounds the sequences: b holds
+                              at most seq_start[b+1] - seq_start[b] tokens (their sum may
+                              pass cap_total).  Needs seq_len (unit_len NULL: the blocks of
+                              a sequence serve every layer and KV head).  Taken by
+                              tria_tree_attention, tria_tree_commit and tria_block_tables;
+                              the other calls return TRIA_ERR_UNSUPPORTED. */
 } tria_cache;
+
+/* A tree of drafted tokens per sequence, as speculative decoding verifies them.  Node i of
+ * sequence b hangs below node parent[b][i] < i, or below the sequence's newest cached token
+ * if that is -1.  A node count outside [0, max_nodes] sets TRIA_DEVERR_TREE and that
+ * sequence is skipped; a parent outside [-1, i) sets it and counts as -1. */
+typedef struct {
+  const int32_t *parent;   /* DEVICE int32 [B][max_nodes]; entries past n_nodes[b] are not read */
+  const int32_t *n_nodes;  /* DEVICE int32 [B] */
+  const void *k;           /* DEVICE bf16 [L][Hkv][B][max_nodes][D], 16-byte aligned: the nodes' */
+  const void *v;           /* post-RoPE keys and their values; rows past n_nodes[b] may hold anything */
+  int32_t max_nodes;       /* 1..TRIA_MAX_NODES */
+} tria_tree;
 
 /* Calibration statistics, DEVICE float32, 16-byte aligned. */
 typedef struct {
@@ -250,6 +295,74 @@ tria_status tria_append(const tria_config *cfg, const tria_cache *cache, const v
 tria_status tria_decode_attention(const tria_config *cfg, const tria_cache *cache, int32_t layer,
                                   const void *q, float scale, float *out, void *ws,
                                   size_t ws_bytes, void *stream);
+
+/* Bytes of workspace for tria_tree_attention and tria_tree_commit with this tree
+ * (no counterpart in the paper; see tria_tree_attention).  Only the shapes are read.  The
+ * start of the workspace (error word, synchronisation words) is laid out as for the other
+ * calls: one workspace of the larger of the two sizes serves them all. */
+tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *cache,
+                                     const tria_tree *tree, size_t *bytes);
+
+/* Attention of drafted trees over the cache: the verification step of speculative
+ * decoding (no counterpart in the paper, whose loop decodes one token at a time; like
+ * tria_decode_attention it reads the budgeted cache, romaanj.github.io review, "Results").
+ * For layer `layer`, every sequence b, node i < n_nodes[b] and query head h (KV head h / G):
+ *   out[b][i][h] = sum_x softmax_x(scale * q[b][i][h] . k_x) v_x
+ * over x in the live cached tokens of (layer, KV head, b) and the nodes of the path from
+ * the tree's root to node i (i included).  A chain (parent[i] = i - 1) makes it the causal
+ * attention of a chunk of prompt tokens, one node that of a single decoded token.  q is
+ * DEVICE bf16 [B][max_nodes][Hq][D], out DEVICE bf16 of the same shape, both 16-byte
+ * aligned; rows past n_nodes[b] are neither read nor written.  scale <= 0 selects
+ * 1/sqrt(D).  What lies in slots past a sequence's length, in blocks that it does not hold
+ * and in other branches of the tree does not reach a result, not even as a NaN.  Sums,
+ * maxima and the output accumulate in float32; the weights are rounded to bf16 for their
+ * product with V, and the output once to bf16.  A seq_len out of range sets
+ * TRIA_DEVERR_SEQ_LEN and that sequence's rows are not written; a block id out of range
+ * sets TRIA_DEVERR_PAGES and leaves that sequence's rows undefined.  ws of at least
+ * tria_tree_workspace_size bytes; it must not overlap another call on the same workspace. */
+tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
+                                const tria_tree *tree, int32_t layer, const void *q, float scale,
+                                void *out, void *ws, size_t ws_bytes, void *stream);
+
+/* The accepted path of every tree joins the cache: tria_append for several tokens (no
+ * counterpart in the paper; the cache grows by decoded tokens as in the romaanj.github.io
+ * review, "Background", here by more than one per step).  last is DEVICE int32 [B]: the
+ * last accepted node of each sequence, or -1 for none.  The K and V rows of the path from
+ * the root to that node, n rows, go to the next n slots of every (layer, KV head) and
+ * their positions cur_pos[b] + 1.. to pos; then seq_len[b] (or every unit's length) and
+ * cur_pos[b] advance by n.  A paged cache takes the slots from slot_map, DEVICE int32
+ * [B][max_new] as tria_block_tables writes it; without pages slot_map is NULL and max_new 0.
+ * A sequence is left unchanged if it has too little room (TRIA_DEVERR_SEGMENT_FULL), a
+ * length out of range (TRIA_DEVERR_SEQ_LEN), an accepted node outside [-1, n_nodes[b]) or
+ * a bad node count (TRIA_DEVERR_TREE), or a slot outside the cache (TRIA_DEVERR_PAGES).
+ * One launch, no host synchronisation.  ws as for tria_tree_attention. */
+tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,
+                             const tria_tree *tree, const int32_t *last, const int32_t *slot_map,
+                             int32_t max_new, void *ws, size_t ws_bytes, void *stream);
+
+/* Brings a paged cache's block tables up to date with the lengths on the GPU, and maps the
+ * next tokens to slots (dimensionstp.github.io review, section 6, Limitations: the pruned
+ * cache in a paged KV cache; a prune shortens sequences on the device, so the host does not
+ * know which blocks they still need).  n_new is DEVICE int32 [B], the tokens that sequence b
+ * is about to add, each in [0, max_new].  With need = ceil((seq_len[b] + n_new[b]) /
+ * block_size) blocks for sequence b:
+ *   - blocks past the need go back to the pool's tail, in the order of (b, place);
+ *   - missing blocks come from its head in the same order, those given back in this call
+ *     included.  Sequences are served in order while the pool covers the demand so far; one
+ *     that it does not cover sets TRIA_DEVERR_POOL and takes none, and so do all after it
+ *     that need any;
+ *   - slot_map, DEVICE int32 [B][max_new], receives the slots of tokens seq_len[b]..
+ *     seq_len[b] + n_new[b] - 1, and -1 after them; a sequence that does not hold the
+ *     blocks for all of them gets -1 throughout.
+ * A sequence whose length or n_new is out of range (TRIA_DEVERR_SEQ_LEN), whose sum passes
+ * its capacity (TRIA_DEVERR_SEGMENT_FULL) or whose held count is out of range
+ * (TRIA_DEVERR_PAGES) keeps its blocks and gets -1s.  A ring_state out of range, or one
+ * whose ring cannot take back what is released, sets TRIA_DEVERR_PAGES and no block changes
+ * hands.  The lengths are only read.  No host synchronisation.  ws: any workspace prepared
+ * by tria_workspace_init (its error word is used); max_new may be 0 and slot_map then NULL. */
+tria_status tria_block_tables(const tria_config *cfg, const tria_cache *cache,
+                              const int32_t *n_new, int32_t max_new, int32_t *slot_map, void *ws,
+                              size_t ws_bytes, void *stream);
 
 /* tria_prune (same passages: romaanj.github.io review, "Method";
  * dimensionstp.github.io review, sections 2-1 and 3-2) with a cudaEvent_t

@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "attention.cuh"
+#include "tree.cuh"
 #include "tria_internal.cuh"
 
 namespace tria {
@@ -127,7 +128,28 @@ tria_status check_config(const tria_config *cfg, bool scoring) {
   return TRIA_OK;
 }
 
-tria_status check_cache(const tria_config *cfg, const tria_cache *c, bool need_kv) {
+// A paged cache (taken by the calls that pass paged_ok).
+tria_status check_pages(const tria_config *cfg, const tria_cache *c) {
+  const tria_pages *pg = c->pages;
+  if (!pg->block_table || !pg->held || !pg->ring || !pg->ring_state) return TRIA_ERR_INVALID_ARG;
+  if (!aligned(pg->block_table, 4) || !aligned(pg->held, 4) || !aligned(pg->ring, 4) ||
+      !aligned(pg->ring_state, 4))
+    return TRIA_ERR_INVALID_ARG;
+  if (pg->n_blocks < 1 || pg->max_blocks < 1 || pg->block_size < 1) return TRIA_ERR_INVALID_ARG;
+  if (pg->block_size < 16 || pg->block_size > 256 || (pg->block_size & (pg->block_size - 1)))
+    return TRIA_ERR_UNSUPPORTED;
+  const int64_t slots = (int64_t)pg->n_blocks * pg->block_size;
+  if (slots > INT32_MAX) return TRIA_ERR_UNSUPPORTED;  // slot maps are int32
+  if (c->cap_total != slots) return TRIA_ERR_INVALID_ARG;
+  if (!c->seq_len || c->unit_len) return TRIA_ERR_INVALID_ARG;
+  for (int b = 0; b < cfg->batch; ++b)
+    if (c->seq_start[b + 1] - c->seq_start[b] > (int64_t)pg->max_blocks * pg->block_size)
+      return TRIA_ERR_INVALID_ARG;
+  return TRIA_OK;
+}
+
+tria_status check_cache(const tria_config *cfg, const tria_cache *c, bool need_kv,
+                        bool paged_ok = false) {
   if (!c) return TRIA_ERR_INVALID_ARG;
   if (!c->seq_start || c->cap_total < 0) return TRIA_ERR_INVALID_ARG;
   // lengths per sequence, or per unit (then seq_len may be null); head budgets need the latter
@@ -146,8 +168,41 @@ tria_status check_cache(const tria_config *cfg, const tria_cache *c, bool need_k
     if (e < a) return TRIA_ERR_INVALID_ARG;
     if (e - a > TRIA_MAX_SEGMENT) return TRIA_ERR_UNSUPPORTED;
   }
+  if (c->pages) return paged_ok ? check_pages(cfg, c) : TRIA_ERR_UNSUPPORTED;
   if (c->seq_start[cfg->batch] > c->cap_total) return TRIA_ERR_INVALID_ARG;
   return TRIA_OK;
+}
+
+tria_status check_tree(const tria_config *cfg, const tria_tree *t, bool need_kv) {
+  if (!t) return TRIA_ERR_INVALID_ARG;
+  if (t->max_nodes < 1) return TRIA_ERR_INVALID_ARG;
+  if (t->max_nodes > TRIA_MAX_NODES) return TRIA_ERR_UNSUPPORTED;
+  if (!need_kv) return TRIA_OK;
+  if (!t->parent || !t->n_nodes || !aligned(t->parent, 4) || !aligned(t->n_nodes, 4))
+    return TRIA_ERR_INVALID_ARG;
+  if (!t->k || !t->v || !aligned(t->k, 16) || !aligned(t->v, 16)) return TRIA_ERR_INVALID_ARG;
+  (void)cfg;
+  return TRIA_OK;
+}
+
+size_t tree_workspace_bytes(const tria_config *cfg, const tria_tree *t) {
+  return kWsPrefix + tree_attention_scratch(cfg->head_dim, cfg->n_q_heads / cfg->n_kv_heads, t->max_nodes);
+}
+
+tria_status check_tree_ws(const tria_config *cfg, const tria_tree *t, void *ws, size_t bytes) {
+  if (!ws || !aligned(ws, 256) || bytes < tree_workspace_bytes(cfg, t)) return TRIA_ERR_WORKSPACE;
+  return TRIA_OK;
+}
+
+PageParams page_params(const tria_cache *c) {
+  PageParams pp{};
+  if (c->pages) {
+    pp.table = c->pages->block_table;
+    pp.max_blocks = c->pages->max_blocks;
+    pp.n_blocks = c->pages->n_blocks;
+    while ((1 << pp.shift) < c->pages->block_size) ++pp.shift;
+  }
+  return pp;
 }
 
 // The score kernel addresses keys by 32-bit tensor coordinates.
@@ -610,6 +665,128 @@ tria_status tria_decode_attention(const tria_config *cfg, const tria_cache *cach
     }
   }
   return cuda_status(launch_attention(ap, static_cast<cudaStream_t>(stream)));
+}
+
+tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *cache,
+                                     const tria_tree *tree, size_t *bytes) {
+  if (!bytes || !cache) return TRIA_ERR_INVALID_ARG;
+  tria_status s = check_config(cfg, false);
+  if (s != TRIA_OK) return s;
+  if ((s = check_tree(cfg, tree, false)) != TRIA_OK) return s;
+  *bytes = tree_workspace_bytes(cfg, tree);
+  return TRIA_OK;
+}
+
+tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
+                                const tria_tree *tree, int32_t layer, const void *q, float scale,
+                                void *out, void *ws, size_t ws_bytes, void *stream) {
+  tria_status s;
+  if ((s = check_config(cfg, false)) != TRIA_OK) return s;
+  if ((s = check_cache(cfg, cache, true, true)) != TRIA_OK) return s;
+  if ((s = check_tree(cfg, tree, true)) != TRIA_OK) return s;
+  if (layer < 0 || layer >= cfg->num_layers) return TRIA_ERR_INVALID_ARG;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return TRIA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return TRIA_ERR_INVALID_ARG;
+  if (!attention_supported(cfg->head_dim, cfg->n_q_heads / cfg->n_kv_heads))
+    return TRIA_ERR_UNSUPPORTED;
+  if ((s = check_tree_ws(cfg, tree, ws, ws_bytes)) != TRIA_OK) return s;
+  TreeAttnParams tp;
+  std::memset(&tp, 0, sizeof tp);
+  tp.parent = tree->parent;
+  tp.n_nodes = tree->n_nodes;
+  tp.q = static_cast<const uint16_t *>(q);
+  tp.k = static_cast<const uint16_t *>(cache->k);
+  tp.v = static_cast<const uint16_t *>(cache->v);
+  tp.kd = static_cast<const uint16_t *>(tree->k);
+  tp.vd = static_cast<const uint16_t *>(tree->v);
+  tp.seq_len = cache->seq_len;
+  tp.unit_len = cache->unit_len;
+  tp.out = static_cast<uint16_t *>(out);
+  tp.err = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsErr);
+  tp.pages = page_params(cache);
+  tp.cap = cache->cap_total;
+  tp.layer = layer;
+  tp.B = cfg->batch;
+  tp.N = tree->max_nodes;
+  tp.Hkv = cfg->n_kv_heads;
+  tp.Hq = cfg->n_q_heads;
+  tp.G = cfg->n_q_heads / cfg->n_kv_heads;
+  tp.D = cfg->head_dim;
+  tp.scale = scale > 0.0f ? scale : 1.0f / std::sqrt((float)cfg->head_dim);
+  for (int b = 0; b <= cfg->batch; ++b) tp.seg_start[b] = cache->seq_start[b];
+  return cuda_status(launch_tree_attention(tp, static_cast<cudaStream_t>(stream)));
+}
+
+tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,
+                             const tria_tree *tree, const int32_t *last, const int32_t *slot_map,
+                             int32_t max_new, void *ws, size_t ws_bytes, void *stream) {
+  tria_status s;
+  if ((s = check_config(cfg, false)) != TRIA_OK) return s;
+  if ((s = check_cache(cfg, cache, true, true)) != TRIA_OK) return s;
+  if ((s = check_tree(cfg, tree, true)) != TRIA_OK) return s;
+  if (!cache->cur_pos || !last || !aligned(last, 4)) return TRIA_ERR_INVALID_ARG;
+  if (cache->pages ? (!slot_map || !aligned(slot_map, 4) || max_new < 1) : (slot_map || max_new))
+    return TRIA_ERR_INVALID_ARG;
+  if (cfg->head_dim > 256) return TRIA_ERR_UNSUPPORTED;
+  if ((s = check_tree_ws(cfg, tree, ws, ws_bytes)) != TRIA_OK) return s;
+  TreeCommitParams cp;
+  std::memset(&cp, 0, sizeof cp);
+  cp.parent = tree->parent;
+  cp.n_nodes = tree->n_nodes;
+  cp.last = last;
+  cp.slot_map = slot_map;
+  cp.k_new = static_cast<const uint8_t *>(tree->k);
+  cp.v_new = static_cast<const uint8_t *>(tree->v);
+  cp.k = static_cast<uint8_t *>(cache->k);
+  cp.v = static_cast<uint8_t *>(cache->v);
+  cp.pos = cache->pos;
+  cp.seq_len = cache->seq_len;
+  cp.unit_len = cache->unit_len;
+  cp.cur_pos = cache->cur_pos;
+  // the arrival counters live in the workspace's zero-at-rest prefix
+  cp.arrived = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsHist);
+  cp.err = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsErr);
+  cp.cap = cache->cap_total;
+  cp.L = cfg->num_layers;
+  cp.Hkv = cfg->n_kv_heads;
+  cp.B = cfg->batch;
+  cp.D = cfg->head_dim;
+  cp.N = tree->max_nodes;
+  cp.max_new = max_new;
+  for (int b = 0; b <= cfg->batch; ++b) cp.seg_start[b] = cache->seq_start[b];
+  return cuda_status(launch_tree_commit(cp, static_cast<cudaStream_t>(stream)));
+}
+
+tria_status tria_block_tables(const tria_config *cfg, const tria_cache *cache,
+                              const int32_t *n_new, int32_t max_new, int32_t *slot_map, void *ws,
+                              size_t ws_bytes, void *stream) {
+  tria_status s;
+  if ((s = check_config(cfg, false)) != TRIA_OK) return s;
+  if (!cache || !cache->pages) return TRIA_ERR_INVALID_ARG;
+  if ((s = check_cache(cfg, cache, false, true)) != TRIA_OK) return s;
+  if (!n_new || !aligned(n_new, 4) || max_new < 0) return TRIA_ERR_INVALID_ARG;
+  if (max_new > TRIA_MAX_SEGMENT) return TRIA_ERR_UNSUPPORTED;
+  if (max_new > 0 && (!slot_map || !aligned(slot_map, 4))) return TRIA_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < 256) return TRIA_ERR_WORKSPACE;
+  BlockTablesParams bp;
+  std::memset(&bp, 0, sizeof bp);
+  const PageParams pp = page_params(cache);
+  bp.table = cache->pages->block_table;
+  bp.held = cache->pages->held;
+  bp.ring = cache->pages->ring;
+  bp.ring_state = cache->pages->ring_state;
+  bp.seq_len = cache->seq_len;
+  bp.n_new = n_new;
+  bp.slot_map = slot_map;
+  bp.err = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsErr);
+  bp.B = cfg->batch;
+  bp.max_new = max_new;
+  bp.max_blocks = pp.max_blocks;
+  bp.n_blocks = pp.n_blocks;
+  bp.shift = pp.shift;
+  for (int b = 0; b < cfg->batch; ++b)
+    bp.seg_cap[b] = (int32_t)(cache->seq_start[b + 1] - cache->seq_start[b]);
+  return cuda_status(launch_block_tables(bp, static_cast<cudaStream_t>(stream)));
 }
 
 tria_status tria_prune_profiled(const tria_config *cfg, const tria_stats *stats,

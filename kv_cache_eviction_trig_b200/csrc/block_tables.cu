@@ -1,0 +1,194 @@
+// Block tables and slot maps of a paged cache from the lengths on the GPU (the pruned cache
+// in a paged KV cache: dimensionstp.github.io review, section 6, Limitations).
+//
+// One block: thread b < B works out what sequence b needs, two prefix sums over the
+// sequences give every block that changes hands its place in the pool's ring, and groups
+// of warps move a sequence's blocks: those past the need to the ring's tail, then, after a
+// barrier, the missing ones from its head.  A second grid (chained by programmatic
+// dependent launch) maps the tokens to slots; few slots are mapped by the first one.
+// Latency bound: the table rows and lengths of a decode step are a few KB.
+#include "tree.cuh"
+
+namespace tria {
+
+namespace {
+
+constexpr int kTableThreads = 1024;
+constexpr int kMapThreads = 256;
+constexpr int64_t kMapInline = 8192;  // slots that the first block maps itself
+
+struct Ask {
+  int32_t len, n;
+  bool ok;  // the length and n are in range and within the sequence's capacity
+};
+
+__device__ __forceinline__ Ask ask_of(const BlockTablesParams &p, int b, int *bad) {
+  Ask a{p.seq_len[b], p.n_new[b], true};
+  const int64_t cap = p.seg_cap[b];
+  *bad = 0;
+  if (a.len < 0 || a.len > cap || a.n < 0 || a.n > p.max_new) *bad = TRIA_DEVERR_SEQ_LEN;
+  else if ((int64_t)a.len + a.n > cap) *bad = TRIA_DEVERR_SEGMENT_FULL;
+  a.ok = *bad == 0;
+  return a;
+}
+
+// Slots of sequence b's next tokens: entries first, first + step, ... of its row.
+__device__ __forceinline__ void map_row(const BlockTablesParams &p, int b, int32_t len, int32_t n,
+                                        bool served, int first, int step) {
+  const int32_t *row = p.table + (int64_t)b * p.max_blocks;
+  int32_t *to = p.slot_map + (int64_t)b * p.max_new;
+  for (int i = first; i < p.max_new; i += step) {
+    int32_t slot = -1;
+    if (served && i < n) {
+      const int32_t t = len + i;
+      slot = (row[t >> p.shift] << p.shift) + (t & ((1 << p.shift) - 1));
+    }
+    to[i] = slot;
+  }
+}
+
+// Inclusive prefix sums of two values over the block's first 256 threads.
+__device__ __forceinline__ void scan2(int32_t (&v)[2], int32_t (*sums)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, v[k], o);
+      if (lane >= o) v[k] += x;
+    }
+  if (lane == 31) {
+    sums[warp][0] = v[0];
+    sums[warp][1] = v[1];
+  }
+  __syncthreads();
+  for (int w = 0; w < warp && w < 8; ++w) {
+    v[0] += sums[w][0];
+    v[1] += sums[w][1];
+  }
+}
+
+__global__ void __launch_bounds__(kTableThreads)
+    block_tables_kernel(const __grid_constant__ BlockTablesParams p, int map_inline) {
+  // per sequence: what it holds, what it gets to hold, its places among the blocks that
+  // are released and taken
+  __shared__ int32_t s_old[TRIA_MAX_BATCH], s_new[TRIA_MAX_BATCH], s_rel[TRIA_MAX_BATCH],
+      s_take[TRIA_MAX_BATCH], s_len[TRIA_MAX_BATCH], s_n[TRIA_MAX_BATCH];
+  __shared__ int32_t sums[kTableThreads / 32][2], totals[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kWarps = kTableThreads / 32;
+  if (tid == 0) dev::pdl_launch_dependents();
+  const int32_t head = p.ring_state[0], count = p.ring_state[1];
+  int32_t old = 0, need = 0, v[2] = {0, 0}, bad = 0;
+  Ask a{0, 0, false};
+  if (tid < p.B) {
+    a = ask_of(p, tid, &bad);
+    old = p.held[tid];
+    if (old < 0 || old > p.max_blocks) {
+      bad |= TRIA_DEVERR_PAGES;
+      a.ok = false;
+    }
+    need = old;
+    if (a.ok) {
+      need = (int32_t)(((int64_t)a.len + a.n + (1 << p.shift) - 1) >> p.shift);
+      v[0] = max(0, old - need);
+      v[1] = max(0, need - old);
+    }
+  }
+  const int32_t rel = v[0], shortage = v[1];
+  scan2(v, sums);
+  if (tid == TRIA_MAX_BATCH - 1) {
+    totals[0] = v[0];
+    totals[1] = v[1];
+  }
+  __syncthreads();
+  const bool ring_ok = head >= 0 && head < p.n_blocks && count >= 0 && count <= p.n_blocks &&
+                       (int64_t)count + totals[0] <= p.n_blocks;
+  const int32_t pool = ring_ok ? count + totals[0] : 0;
+  if (tid < p.B) {
+    if (!ring_ok) need = old;
+    else if (shortage > 0 && v[1] > pool) {
+      bad |= TRIA_DEVERR_POOL;
+      need = old;
+    }
+    s_old[tid] = old;
+    s_new[tid] = need;
+    s_rel[tid] = v[0] - rel;
+    s_take[tid] = v[1] - shortage;
+    s_len[tid] = a.len;
+    s_n[tid] = a.ok && (int64_t)a.len + a.n <= ((int64_t)need << p.shift) ? a.n : -1;
+  }
+  if (tid == 0 && !ring_ok) bad |= TRIA_DEVERR_PAGES;
+  if (bad) dev::set_error(p.err, bad);
+  __syncthreads();
+  // a group of warps per sequence
+  const int per = max(1, kWarps / p.B), group = warp / per, groups = kWarps / per;
+  const int first = (warp - group * per) * 32 + lane, step = per * 32;
+  for (int b = group; b < p.B; b += groups) {
+    const int32_t n0 = s_new[b], n1 = s_old[b];
+    if (n1 <= n0) continue;
+    int32_t *row = p.table + (int64_t)b * p.max_blocks;
+    for (int j = n0 + first; j < n1; j += step) {
+      const int64_t at = (int64_t)head + count + s_rel[b] + (j - n0);
+      p.ring[at % p.n_blocks] = row[j];
+      row[j] = -1;
+    }
+  }
+  __syncthreads();  // what was released can be taken
+  for (int b = group; b < p.B; b += groups) {
+    const int32_t n0 = s_old[b], n1 = s_new[b];
+    int32_t *row = p.table + (int64_t)b * p.max_blocks;
+    for (int j = n0 + first; j < n1; j += step) {
+      const int64_t at = (int64_t)head + s_take[b] + (j - n0);
+      const int32_t id = p.ring[at % p.n_blocks];
+      if (id < 0 || id >= p.n_blocks) dev::set_error(p.err, TRIA_DEVERR_PAGES);
+      row[j] = id;
+    }
+  }
+  if (tid < p.B) p.held[tid] = s_new[tid];
+  __syncthreads();  // the rows are complete
+  if (warp == 0) {
+    int32_t all = 0;
+    for (int b = lane; b < p.B; b += 32) all += max(0, s_new[b] - s_old[b]);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0 && ring_ok) {
+      p.ring_state[0] = (int32_t)(((int64_t)head + all) % p.n_blocks);
+      p.ring_state[1] = pool - all;
+    }
+  }
+  if (!map_inline) return;
+  for (int b = group; b < p.B; b += groups) map_row(p, b, s_len[b], s_n[b], s_n[b] >= 0, first, step);
+}
+
+__global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const __grid_constant__ BlockTablesParams p) {
+  dev::pdl_wait();
+  const int b = blockIdx.y;
+  int bad;
+  const Ask a = ask_of(p, b, &bad);
+  const int32_t held = p.held[b];
+  const bool served = a.ok && held >= 0 && held <= p.max_blocks &&
+                      (int64_t)a.len + a.n <= ((int64_t)held << p.shift);
+  map_row(p, b, a.len, a.n, served, blockIdx.x * kMapThreads + threadIdx.x, gridDim.x * kMapThreads);
+}
+
+}  // namespace
+
+cudaError_t launch_block_tables(const BlockTablesParams &p, cudaStream_t s) {
+  const bool small = (int64_t)p.B * p.max_new <= kMapInline;
+  block_tables_kernel<<<1, kTableThreads, 0, s>>>(p, small ? 1 : 0);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || small) return e;
+  const int64_t per = ((int64_t)p.max_new + kMapThreads - 1) / kMapThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(per < 1024 ? per : 1024), (unsigned)p.B, 1);
+  cfg.blockDim = dim3(kMapThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, slot_map_kernel, p);
+}
+
+}  // namespace tria

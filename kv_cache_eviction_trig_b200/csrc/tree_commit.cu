@@ -1,0 +1,119 @@
+// The accepted path of every drafted tree joins the cache: tria_append for several tokens
+// per sequence (the cache grows by decoded tokens, romaanj.github.io review, "Background";
+// the paper decodes one at a time).
+//
+// A block takes one sequence and kLgPerBlock of its (layer, KV head) rows.  It brings the
+// sequence's parents into shared memory, walks from the accepted node to the root, and its
+// warps copy the path's K and V rows (16-byte vectors, a warp per row pair) to the next
+// slots; every block reads the length before it reports, and the sequence's last block to
+// report advances the lengths, so the step is one launch.  A sequence that cannot take its
+// path is left as it is by every block, for the same reason.
+// Bound by the rows' bytes (8 D + 4 per token and (layer, KV head) row).
+#include "tree.cuh"
+
+namespace tria {
+
+namespace {
+
+constexpr int kCommitThreads = 256;
+constexpr int kLgPerBlock = 8;
+
+__global__ void __launch_bounds__(kCommitThreads)
+    tree_commit_kernel(const __grid_constant__ TreeCommitParams p) {
+  __shared__ int32_t parent[TRIA_MAX_NODES];
+  __shared__ int32_t path[TRIA_MAX_NODES];  // leaf first
+  __shared__ int32_t depth;
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t rows = (int64_t)p.L * p.Hkv;
+  const int64_t cap_b = p.seg_start[b + 1] - p.seg_start[b];
+  const int32_t last = p.last[b], n = p.n_nodes[b];
+  int bad = n < 0 || n > p.N || last < -1 || last >= n ? TRIA_DEVERR_TREE : 0;
+  if (bad || last < 0) {  // the same decision in every block of the sequence
+    if (bad && blockIdx.y == 0 && tid == 0) dev::set_error(p.err, bad);
+    return;
+  }
+  for (int i = tid; i <= last; i += kCommitThreads) {
+    const int32_t up = p.parent[(int64_t)b * p.N + i];
+    const bool fine = up >= -1 && up < i;
+    if (!fine && blockIdx.y == 0) dev::set_error(p.err, TRIA_DEVERR_TREE);
+    parent[i] = fine ? up : -1;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int d = 0;
+    for (int i = last; i >= 0; i = parent[i]) path[d++] = i;  // parents precede their children
+    depth = d;
+  }
+  __syncthreads();
+  const int len = depth;
+  if (p.unit_len) {
+    for (int64_t lg = tid; lg < rows; lg += kCommitThreads) {
+      const int32_t T = p.unit_len[lg * p.B + b];
+      if (T < 0 || (int64_t)T > cap_b) bad |= TRIA_DEVERR_SEQ_LEN;
+      else if ((int64_t)T + len > cap_b) bad |= TRIA_DEVERR_SEGMENT_FULL;
+    }
+  } else {
+    const int32_t T = p.seq_len[b];
+    if (T < 0 || (int64_t)T > cap_b) bad = TRIA_DEVERR_SEQ_LEN;
+    else if ((int64_t)T + len > cap_b) bad = TRIA_DEVERR_SEGMENT_FULL;
+  }
+  if (p.slot_map) {
+    if (len > p.max_new) bad |= TRIA_DEVERR_PAGES;
+    for (int j = tid; j < len && j < p.max_new; j += kCommitThreads) {
+      const int32_t s = p.slot_map[(int64_t)b * p.max_new + j];
+      if (s < 0 || (int64_t)s >= p.cap) bad |= TRIA_DEVERR_PAGES;
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (blockIdx.y == 0 && bad) dev::set_error(p.err, bad);
+    return;
+  }
+  const int nv = p.D >> 3;  // 16-byte vectors per row
+  const int32_t cur = p.cur_pos[b];
+  for (int64_t lg = (int64_t)blockIdx.y * kLgPerBlock + warp;
+       lg < rows && lg < (int64_t)(blockIdx.y + 1) * kLgPerBlock; lg += kCommitThreads / 32) {
+    const int64_t T = p.slot_map ? 0 : p.seg_start[b] + (p.unit_len ? p.unit_len[lg * p.B + b] : p.seq_len[b]);
+    const uint4 *ks = reinterpret_cast<const uint4 *>(p.k_new) + (lg * p.B + b) * p.N * nv;
+    const uint4 *vs = reinterpret_cast<const uint4 *>(p.v_new) + (lg * p.B + b) * p.N * nv;
+    uint4 *kd = reinterpret_cast<uint4 *>(p.k) + lg * p.cap * nv;
+    uint4 *vd = reinterpret_cast<uint4 *>(p.v) + lg * p.cap * nv;
+    for (int j = 0; j < len; ++j) {
+      const int64_t slot = p.slot_map ? p.slot_map[(int64_t)b * p.max_new + j] : T + j;
+      const int64_t node = path[len - 1 - j];
+      for (int i = lane; i < 2 * nv; i += 32) {
+        if (i < nv) kd[slot * nv + i] = ks[node * nv + i];
+        else vd[slot * nv + i - nv] = vs[node * nv + i - nv];
+      }
+      if (lane == 0) p.pos[lg * p.cap + slot] = cur + 1 + j;
+    }
+  }
+  // the sequence's last block advances its lengths: the others have read them
+  __syncthreads();
+  __shared__ int mine;
+  if (tid == 0) {
+    __threadfence();
+    mine = atomicAdd(p.arrived + b, 1) == (int)gridDim.y - 1;
+  }
+  __syncthreads();
+  if (!mine) return;
+  if (p.unit_len) {
+    for (int64_t lg = tid; lg < rows; lg += kCommitThreads) p.unit_len[lg * p.B + b] += len;
+  } else if (tid == 0) {
+    p.seq_len[b] += len;
+  }
+  if (tid == 0) {
+    p.cur_pos[b] = cur + len;
+    p.arrived[b] = 0;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t s) {
+  const int64_t chunks = ((int64_t)p.L * p.Hkv + kLgPerBlock - 1) / kLgPerBlock;
+  if (chunks > 65535) return cudaErrorInvalidValue;
+  tree_commit_kernel<<<dim3((unsigned)p.B, (unsigned)chunks), kCommitThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace tria

@@ -32,6 +32,7 @@ DTYPE_BF16 = 1
 MAX_BATCH = 256
 MAX_OFFSETS = 4096
 MAX_SEGMENT = 1 << 18
+MAX_NODES = 256
 PRUNE_MAX_STAGES = 8
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -41,11 +42,16 @@ DEVERR_TIMEOUT = 4
 DEVERR_SEGMENT_BIG = 8
 DEVERR_SEGMENT_FULL = 16
 DEVERR_BUDGET = 32
+DEVERR_TREE = 64
+DEVERR_PAGES = 128
+DEVERR_POOL = 256
 
 EXPORTS = ["tria_workspace_size", "tria_workspace_init", "tria_calibrate", "tria_score",
            "tria_select", "tria_compact", "tria_prune", "tria_prune_profiled",
            "tria_prune_stage_name", "tria_get_device_error", "tria_status_string", "tria_version",
-           "tria_prune_noalloc", "tria_append", "tria_decode_attention"]
+           "tria_prune_noalloc", "tria_append", "tria_decode_attention",
+           "tria_tree_workspace_size", "tria_tree_attention", "tria_tree_commit",
+           "tria_block_tables"]
 
 
 class TriaError(RuntimeError):
@@ -64,11 +70,23 @@ class tria_config(ctypes.Structure):
                 ("head_budgets", ctypes.c_void_p)]
 
 
+class tria_pages(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("ring", ctypes.c_void_p), ("ring_state", ctypes.c_void_p),
+                ("block_size", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32)]
+
+
 class tria_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pos", ctypes.c_void_p),
                 ("seq_len", ctypes.c_void_p), ("cur_pos", ctypes.c_void_p),
                 ("seq_start", ctypes.POINTER(ctypes.c_int64)), ("cap_total", ctypes.c_int64),
-                ("unit_len", ctypes.c_void_p)]
+                ("unit_len", ctypes.c_void_p), ("pages", ctypes.POINTER(tria_pages))]
+
+
+class tria_tree(ctypes.Structure):
+    _fields_ = [("parent", ctypes.c_void_p), ("n_nodes", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("max_nodes", ctypes.c_int32)]
 
 
 class tria_stats(ctypes.Structure):
@@ -107,6 +125,15 @@ def lib():
         L.tria_append.argtypes = [P(tria_config), P(tria_cache), vp, vp, vp, ctypes.c_size_t, vp]
         L.tria_decode_attention.argtypes = [P(tria_config), P(tria_cache), ctypes.c_int32, vp,
                                             ctypes.c_float, vp, vp, ctypes.c_size_t, vp]
+        L.tria_tree_workspace_size.argtypes = [P(tria_config), P(tria_cache), P(tria_tree),
+                                               P(ctypes.c_size_t)]
+        L.tria_tree_attention.argtypes = [P(tria_config), P(tria_cache), P(tria_tree),
+                                          ctypes.c_int32, vp, ctypes.c_float, vp, vp,
+                                          ctypes.c_size_t, vp]
+        L.tria_tree_commit.argtypes = [P(tria_config), P(tria_cache), P(tria_tree), vp, vp,
+                                       ctypes.c_int32, vp, ctypes.c_size_t, vp]
+        L.tria_block_tables.argtypes = [P(tria_config), P(tria_cache), vp, ctypes.c_int32, vp, vp,
+                                        ctypes.c_size_t, vp]
         L.tria_prune_stage_name.argtypes = [ctypes.c_int32]
         L.tria_prune_stage_name.restype = ctypes.c_char_p
         L.tria_get_device_error.argtypes = [vp, P(ctypes.c_int32), vp]
@@ -169,24 +196,71 @@ class Config:
                    prune_window=prune_window, head_budgets=head_budgets)
 
 
+def _want(t: torch.Tensor, dtype, shape, what: str):
+    """A tensor's pointer, after a check that it is what the call reads or writes."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+class Pages:
+    """tria_pages over int32 device tensors: block_table [B][max_blocks], held [B], ring
+    [n_blocks] and ring_state [2] (head, free); see include/tria.h for how they start."""
+
+    def __init__(self, block_table: torch.Tensor, held: torch.Tensor, ring: torch.Tensor,
+                 ring_state: torch.Tensor, block_size: int):
+        B, max_blocks = block_table.shape
+        self.tensors = (block_table, held, ring, ring_state)
+        self.block_size = block_size
+        self.c = tria_pages(_want(block_table, torch.int32, (B, max_blocks), "block_table"),
+                            _want(held, torch.int32, (B,), "held"),
+                            _want(ring, torch.int32, (ring.numel(),), "ring"),
+                            _want(ring_state, torch.int32, (2,), "ring_state"),
+                            block_size, ring.numel(), max_blocks)
+
+    @classmethod
+    def empty(cls, batch: int, max_blocks: int, n_blocks: int, block_size: int,
+              device="cuda") -> "Pages":
+        """No sequence holds a block; the pool holds them all."""
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((batch, max_blocks), -1, **i32), torch.zeros(batch, **i32),
+                   torch.arange(n_blocks, **i32), torch.tensor([0, n_blocks], **i32), block_size)
+
+
 class Cache:
     """tria_cache over torch tensors (k, v bf16 [L][Hkv][cap][D]; pos int32 [L][Hkv][cap];
     seq_len, cur_pos int32 [B] on the device; seq_start a host list of B+1 ints;
-    optionally unit_len int32 [L][Hkv][B], the per-unit live lengths)."""
+    optionally unit_len int32 [L][Hkv][B], the per-unit live lengths, or pages)."""
 
     def __init__(self, k, v, pos, seq_len, cur_pos, seq_start: Sequence[int],
-                 cap_total: Optional[int] = None, unit_len=None):
+                 cap_total: Optional[int] = None, unit_len=None, pages: Optional[Pages] = None):
         self.tensors = (k, v, pos, seq_len, cur_pos, unit_len)
+        self.pages = pages
         self._starts = (ctypes.c_int64 * len(seq_start))(*seq_start)
         cap = cap_total if cap_total is not None else (k.shape[2] if k is not None else 0)
         self.c = tria_cache(_ptr(k), _ptr(v), _ptr(pos), _ptr(seq_len), _ptr(cur_pos),
                             ctypes.cast(self._starts, ctypes.POINTER(ctypes.c_int64)), cap,
-                            _ptr(unit_len))
+                            _ptr(unit_len), ctypes.pointer(pages.c) if pages else None)
 
     @classmethod
     def from_data(cls, data: dict) -> "Cache":
         return cls(data["k"], data["v"], data["pos"], data["seq_len"], data["cur_pos"],
                    data["seq_start"])
+
+
+class Tree:
+    """tria_tree over device tensors: parent int32 [B][N], n_nodes int32 [B], and the drafted
+    nodes' post-RoPE keys and values k, v bf16 [L][Hkv][B][N][D]."""
+
+    def __init__(self, parent: torch.Tensor, n_nodes: torch.Tensor, k: torch.Tensor,
+                 v: torch.Tensor):
+        B, N = parent.shape
+        L, Hkv, _, _, D = self.shape = tuple(k.shape)
+        self.tensors = (parent, n_nodes, k, v)
+        self.c = tria_tree(_want(parent, torch.int32, (B, N), "parent"),
+                           _want(n_nodes, torch.int32, (B,), "n_nodes"),
+                           _want(k, torch.bfloat16, (L, Hkv, B, N, D), "k"),
+                           _want(v, torch.bfloat16, (L, Hkv, B, N, D), "v"), N)
 
 
 class Stats:
@@ -204,9 +278,21 @@ def tria_workspace_size(cfg: Config, cache: Cache) -> int:
     return int(n.value)
 
 
-def workspace(cfg: Config, cache: Cache, device=None, stream=None) -> torch.Tensor:
-    """Allocates (with torch) and initialises a workspace for this problem."""
+def tria_tree_workspace_size(cfg: Config, cache: Cache, tree: Tree) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().tria_tree_workspace_size(ctypes.byref(cfg.c), ctypes.byref(cache.c),
+                                          ctypes.byref(tree.c), ctypes.byref(n)),
+           "tria_tree_workspace_size")
+    return int(n.value)
+
+
+def workspace(cfg: Config, cache: Cache, device=None, stream=None,
+              tree: Optional[Tree] = None) -> torch.Tensor:
+    """Allocates (with torch) and initialises a workspace for this problem: for the calls
+    without a tree, or for those and the calls with this one."""
     n = tria_workspace_size(cfg, cache)
+    if tree is not None:
+        n = max(n, tria_tree_workspace_size(cfg, cache, tree))
     ws = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + n]
@@ -276,6 +362,53 @@ def tria_decode_attention(cfg: Config, cache: Cache, layer: int, q: torch.Tensor
     _check(lib().tria_decode_attention(ctypes.byref(cfg.c), ctypes.byref(cache.c), layer,
                                        _ptr(q), ctypes.c_float(scale), _ptr(out), _ptr(ws),
                                        ws.numel(), _stream(stream)), "tria_decode_attention")
+
+
+def _check_tree(cfg: Config, tree: Tree):
+    c = cfg.c
+    want = (c.num_layers, c.n_kv_heads, c.batch, tree.c.max_nodes, c.head_dim)
+    if tree.shape != want:
+        raise ValueError(f"the tree's keys are {tree.shape}, the configuration's {want}")
+
+
+def tria_tree_attention(cfg: Config, cache: Cache, tree: Tree, layer: int, q: torch.Tensor,
+                        out: torch.Tensor, ws: torch.Tensor, scale: Optional[float] = None,
+                        stream=None):
+    """q, out: bf16 [B][N][Hq][D] device tensors; rows past a sequence's nodes are neither
+    read nor written; scale None (or <= 0) lets the library use 1/sqrt(D)."""
+    _check_tree(cfg, tree)
+    rows = (cfg.c.batch, tree.c.max_nodes, cfg.c.n_q_heads, cfg.c.head_dim)
+    _check(lib().tria_tree_attention(
+        ctypes.byref(cfg.c), ctypes.byref(cache.c), ctypes.byref(tree.c), layer,
+        _want(q, torch.bfloat16, rows, "q"), 0.0 if scale is None else scale,
+        _want(out, torch.bfloat16, rows, "out"), _ptr(ws), ws.numel(), _stream(stream)),
+        "tria_tree_attention")
+
+
+def tria_tree_commit(cfg: Config, cache: Cache, tree: Tree, last: torch.Tensor, ws: torch.Tensor,
+                     slot_map: Optional[torch.Tensor] = None, stream=None):
+    """last: int32 [B], each sequence's last accepted node or -1; slot_map: int32 [B][max_new]
+    as tria_block_tables wrote it, for a paged cache."""
+    _check_tree(cfg, tree)
+    B = cfg.c.batch
+    max_new = 0 if slot_map is None else slot_map.shape[1]
+    _check(lib().tria_tree_commit(
+        ctypes.byref(cfg.c), ctypes.byref(cache.c), ctypes.byref(tree.c),
+        _want(last, torch.int32, (B,), "last"),
+        None if slot_map is None else _want(slot_map, torch.int32, (B, max_new), "slot_map"),
+        max_new, _ptr(ws), ws.numel(), _stream(stream)), "tria_tree_commit")
+
+
+def tria_block_tables(cfg: Config, cache: Cache, n_new: torch.Tensor,
+                      slot_map: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
+    """n_new: int32 [B], the tokens each sequence is about to add; slot_map: int32
+    [B][max_new], or None to update the tables alone (n_new is then all 0)."""
+    B = cfg.c.batch
+    max_new = 0 if slot_map is None else slot_map.shape[1]
+    _check(lib().tria_block_tables(
+        ctypes.byref(cfg.c), ctypes.byref(cache.c), _want(n_new, torch.int32, (B,), "n_new"),
+        max_new, None if slot_map is None else _want(slot_map, torch.int32, (B, max_new), "slot_map"),
+        _ptr(ws), ws.numel(), _stream(stream)), "tria_block_tables")
 
 
 def tria_prune_profiled(cfg: Config, stats: Stats, cache: Cache, ws: torch.Tensor, events,

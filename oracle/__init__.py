@@ -334,5 +334,88 @@ def decode_attention(k: np.ndarray, v: np.ndarray, seq_start: Sequence[int],
     return out
 
 
+def tree_path(parent: Sequence[int], node: int) -> list:
+    """The path from a drafted tree's root to `node` (both included); node -1 gives none.
+    A parent outside [-1, node) counts as -1."""
+    out = []
+    while node >= 0:
+        out.append(node)
+        up = int(parent[node])
+        node = up if -1 <= up < node else -1
+    return out[::-1]
+
+
+def tree_attention(k: np.ndarray, v: np.ndarray, slots: Sequence, kd: np.ndarray, vd: np.ndarray,
+                   parent: np.ndarray, n_nodes: Sequence[int], q: np.ndarray, layer: int,
+                   scale: float):
+    """Attention of drafted trees over the cache, in float64: node i of sequence b and query
+    head h see the cached tokens of slots[b][h // G] and the nodes of the path to i,
+        out[b, i, h] = sum_x softmax_x(scale * q[b, i, h] . k_x) v_x.
+    k, v: uint16 bf16 bits [L][Hkv][cap][D]; kd, vd: [L][Hkv][B][N][D]; q: [B][N][Hq][D].
+    -> (out, spread, steep), float64: `spread` is sum_x softmax_x |v_x| and `steep` the
+    largest scale * sum_d |q_d k_xd| over the seen keys, which bound what rounding the
+    weights and the products can change.  NaN where i >= n_nodes[b]."""
+    def f64(bits):
+        return (np.asarray(bits, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)
+    B, N, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    out = np.full((B, N, Hq, D), np.nan)
+    spread, steep = np.full((B, N, Hq, D), np.nan), np.full((B, N, Hq), np.nan)
+    for b in range(B):
+        for g in range(k.shape[1]):
+            K0, V0 = f64(k[layer, g, slots[b][g]]), f64(v[layer, g, slots[b][g]])
+            for i in range(int(n_nodes[b])):
+                path = tree_path(parent[b], i)
+                K = np.concatenate([K0, f64(kd[layer, g, b, path])])
+                V = np.concatenate([V0, f64(vd[layer, g, b, path])])
+                Q = f64(q[b, i, g * G:(g + 1) * G])
+                x = scale * (Q @ K.T)
+                w = np.exp(x - x.max(1, keepdims=True))
+                w /= w.sum(1, keepdims=True)
+                out[b, i, g * G:(g + 1) * G] = w @ V
+                spread[b, i, g * G:(g + 1) * G] = w @ np.abs(V)
+                steep[b, i, g * G:(g + 1) * G] = scale * (np.abs(Q) @ np.abs(K).T).max(1)
+    return out, spread, steep
+
+
+def block_tables(table: np.ndarray, held: Sequence[int], ring: np.ndarray, state: Sequence[int],
+                 block: int, lens: Sequence[int], n_new: Sequence[int], caps: Sequence[int],
+                 max_new: int):
+    """Block tables brought up to date, one block at a time: each sequence gives back what
+    lies past its need (to the ring's tail), then takes what is missing from the ring's head
+    while the pool covers the demand of the sequences so far.  -> table, held, ring, state,
+    slot map [B][max_new], and the sequences that were skipped: {b: "length", "full", "pool"}."""
+    table, ring = table.copy(), ring.copy()
+    held, (head, count) = [int(x) for x in held], [int(x) for x in state]
+    B, n = len(held), len(ring)
+    skipped, need = {}, list(held)
+    for b in range(B):
+        if lens[b] < 0 or lens[b] > caps[b] or not 0 <= n_new[b] <= max_new:
+            skipped[b] = "length"
+        elif lens[b] + n_new[b] > caps[b]:
+            skipped[b] = "full"
+        else:
+            need[b] = -(-(int(lens[b]) + int(n_new[b])) // block)
+        for j in range(need[b], held[b]):
+            ring[(head + count) % n], table[b, j] = table[b, j], -1
+            count += 1
+        held[b] = min(held[b], need[b])
+    pool, wanted = count, 0
+    for b in range(B):
+        wanted += need[b] - held[b]
+        if need[b] > held[b] and wanted > pool:
+            skipped[b] = "pool"
+            continue
+        while held[b] < need[b]:
+            table[b, held[b]] = ring[head]
+            head, count, held[b] = (head + 1) % n, count - 1, held[b] + 1
+    slots = np.full((B, max_new), -1, dtype=np.int32)
+    for b in range(B):
+        for i in range(0 if b in skipped else int(n_new[b])):
+            t = int(lens[b]) + i
+            slots[b, i] = table[b, t // block] * block + t % block
+    return table, held, ring, [head, count], slots, skipped
+
+
 def num_threads() -> int:
     return int(lib().orc_num_threads())

@@ -706,6 +706,7 @@ tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
   tp.pages = page_params(cache);
   tp.cap = cache->cap_total;
   tp.layer = layer;
+  tp.L = cfg->num_layers;
   tp.B = cfg->batch;
   tp.N = tree->max_nodes;
   tp.Hkv = cfg->n_kv_heads;
@@ -714,7 +715,8 @@ tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
   tp.D = cfg->head_dim;
   tp.scale = scale > 0.0f ? scale : 1.0f / std::sqrt((float)cfg->head_dim);
   for (int b = 0; b <= cfg->batch; ++b) tp.seg_start[b] = cache->seq_start[b];
-  return cuda_status(launch_tree_attention(tp, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_tree_attention(tp, static_cast<uint8_t *>(ws) + kWsPrefix,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,

@@ -48,7 +48,18 @@ struct TreeCommitParams {
 };
 cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t s);
 
+// What a CTA of the attention leaves for the merge: the unit that its share of the tiles
+// ends in, if that goes on in the next CTAs.
+struct alignas(32) TreeDesc {
+  int32_t b, g, mg, n, last;  // b < 0: none; last: the CTA where the unit ends
+};
+
 struct alignas(64) TreeAttnParams {
+  CUtensorMap tk, tv;       // K and V as [L*Hkv][cap][D], boxes of 64 columns x 128 rows (or a block)
+  CUtensorMap tkd, tvd;     // the nodes' as [L*Hkv*B][N][D], boxes of 64 x draft_rows
+  CUtensorMap tq;           // the queries as [B*N][Hq][D], boxes of 64 x G heads x 128 / G nodes
+  TreeDesc *desc;           // one per CTA
+  float *scratch;           // two parts per CTA: unnormalised output [D][rows], maxima, sums
   const int32_t *parent;    // [B][N]
   const int32_t *n_nodes;   // [B]
   const uint16_t *q;        // bf16 [B][N][Hq][D]
@@ -62,12 +73,13 @@ struct alignas(64) TreeAttnParams {
   int32_t *err;
   PageParams pages;
   int64_t cap;
-  int32_t layer, B, N, Hkv, Hq, G, D;
+  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows;
   float scale;
   int64_t seg_start[TRIA_MAX_BATCH + 1];
 };
-cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t s);
-// Bytes of scratch that the launch needs behind the workspace's fixed prefix.
+// The tensor maps and what depends on the launch are filled in here; scratch holds
+// tree_attention_scratch bytes.
+cudaError_t launch_tree_attention(const TreeAttnParams &p, void *scratch, cudaStream_t s);
 size_t tree_attention_scratch(int D, int G, int N);
 
 }  // namespace tria

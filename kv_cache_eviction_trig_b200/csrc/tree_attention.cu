@@ -4,128 +4,831 @@
 //   out[b][i][h] = sum_x softmax_x(scale * q[b][i][h] . k_x) v_x
 // over the live cached tokens and the nodes on the path from the root to i.
 //
-// One warp per (sequence, node, query head): 32 keys at a time, a lane per key for the
-// products with the query, then a lane per D / 32 output dims for those with V; a running
-// maximum and sum (online softmax), float32 throughout.
+// Design (sm_100a).  The G heads of a group share keys, so the rows of one product are
+// (node, head) pairs: 128 of them per M tile.  A unit is (sequence, KV head, group of MT M
+// tiles); its keys come in tiles of 128, the cached ones first, the drafted nodes last.  The
+// host does not know the lengths, so every CTA adds them up and takes an equal share of the
+// list of all units' tiles (a persistent grid, one CTA per SM), whatever unit it starts or
+// ends in.  Within a CTA
+//   warp 0        streams K and V tiles into a shared-memory ring by TMA (128-byte swizzle;
+//                 a box per block of a paged cache), and the units' queries;
+//   warp 1        one thread issues the tensor products: S = Q K^T into tensor memory, and
+//                 O += P V with P read from tensor memory, where it overlays S;
+//   warps 4..     a warpgroup per M tile, a thread per row: S from tensor memory, the
+//                 running maximum and sum, P = 2^(S - m) as bf16 back to tensor memory.
+// The next tile's S is computed while this one's softmax runs (MT = 1: two S buffers; MT = 2:
+// the M tiles alternate).  O stays in tensor memory and is rescaled only when a row's
+// maximum grew by more than 2^8 (P is at most 2^8 then; float32 sums lose nothing).
+// A unit that lies in one CTA is written from there; the parts of the others go to the
+// workspace with their maxima and sums, and a second kernel (chained by programmatic
+// dependent launch) merges them in the order of the keys, so results do not depend on timing.
+//
+// Rounding: S, maxima, sums and O are float32.  P is rounded to bf16 for the product with
+// the bf16 V (its error is that of the bf16 output's own rounding); the sum is of the
+// unrounded P.
+//
+// Masks.  Columns past the length, and nodes off a row's path, are set to -inf in S.  V rows
+// past the length are zeroed in shared memory (P is 0 there, but 0 * NaN is not), and
+// so are Inf and NaN in the drafted V rows; the rows that do see such a node get them back
+// in the epilogue.
+//
+// What bounds it: K and V bytes for up to about 256 rows per KV head, the products above.
 #include <cuda_bf16.h>
 #include <math.h>
+#include <mutex>
 
+#include <cudaTypedefs.h>
+
+#include "mma_sync.cuh"
+#include "tcgen05.cuh"
 #include "tree.cuh"
 
 namespace tria {
 
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kTile = 128;   // keys per tile, rows per M tile
+constexpr int kPartSlots = 2;  // parts that a CTA can leave: of its first and of its last unit
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+template <int D, int MT>
+struct TreeShape {
+  static constexpr int TB = kTile * D * 2;               // a K or V tile, or an M tile of queries
+  static constexpr int SLAB = kTile * 128;               // 128 rows of 64 columns
+  static constexpr int QB = D == 256 || (D == 128 && MT == 2) ? 1 : 2;  // query buffers
+  static constexpr int NS = D == 256 ? 2 : D == 64 ? 8 : MT == 2 ? 4 : 5;  // ring slots
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = QB * MT * TB;
+  static constexpr int OFF_CTL = OFF_RING + NS * TB;
+  static constexpr int THREADS = 128 + 128 * MT;
+};
 
-template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32)
-    tree_rows_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int E = D / 32;
-  __shared__ float qs[kRowWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kRowWarps + warp;  // (b * N + i) * Hq + h
-  if (row >= (int64_t)p.B * p.N * p.Hq) return;
-  const int h = (int)(row % p.Hq), i = (int)(row / p.Hq % p.N), b = (int)(row / p.Hq / p.N);
-  const int g = h / p.G;
-  const int64_t lg = (int64_t)p.layer * p.Hkv + g;
-  const int32_t n = p.n_nodes[b];
-  const int32_t T = p.unit_len ? p.unit_len[lg * p.B + b] : p.seq_len[b];
-  int bad = 0;
-  if (n < 0 || n > p.N) bad |= TRIA_DEVERR_TREE;
-  if (T < 0 || (int64_t)T > p.seg_start[b + 1] - p.seg_start[b]) bad |= TRIA_DEVERR_SEQ_LEN;
-  if (bad || i >= n) {
-    if (bad && i == 0 && lane == 0) dev::set_error(p.err, bad);
-    return;
+struct TreeCtl {
+  uint64_t full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], done;
+  uint32_t tmem;
+  int32_t abort;
+  int32_t start_b, start_rem;          // where this CTA's share starts
+  int32_t warp_sums[8];
+  uint32_t poison[4];                  // drafted V rows of the tile with Inf or NaN
+  uint32_t tn[TRIA_MAX_BATCH];         // live length (0 with per-unit lengths) << 9 | nodes (0: skipped)
+  int16_t parent[TRIA_MAX_NODES];
+};
+static_assert(TRIA_MAX_NODES < 512 && TRIA_MAX_SEGMENT < (1 << 23), "lengths and nodes in one word");
+
+template <int D, int MT>
+constexpr int tree_smem() {
+  return TreeShape<D, MT>::OFF_CTL + (int)sizeof(TreeCtl) + 1024;  // + room to align to 1024
+}
+
+// Waits that ran out make every later wait return at once; all roles then run through
+// their loops without issuing copies or products.
+__device__ __forceinline__ bool tree_wait(TreeCtl &c, uint64_t *bar, uint32_t parity, int32_t *err) {
+  if (dev::mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < 2000000u; ++i) {
+    if (*reinterpret_cast<volatile int32_t *>(&c.abort)) return false;
+    if (dev::mbar_try_wait(bar, parity)) return true;
   }
-  for (int d = lane; d < D; d += 32) qs[warp][d] = bf(p.q[row * D + d]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.0f, o[E] = {};
-  // one group of 32 keys: key rows kr, value rows vr (null: not seen)
-  auto take = [&](const uint16_t *kr, const uint16_t *vr) {
-    float s = -INFINITY;
-    if (kr) {
-      s = 0.0f;
-      for (int d = 0; d < D; ++d) s = fmaf(bf(kr[d]), qs[warp][d], s);
-      s *= p.scale;
-    }
-    float mx = s;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) return;
-    const float a = expf(m - mn), w = kr ? expf(s - mn) : 0.0f;
-    float sum = w;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * a + sum;
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= a;
-    for (int x = 0; x < 32; ++x) {
-      const uint16_t *v = reinterpret_cast<const uint16_t *>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vr), x));
-      const float wx = __shfl_sync(0xffffffffu, w, x);
-      if (!v) continue;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(wx, bf(v[lane + 32 * e]), o[e]);
-    }
-  };
-  for (int t0 = 0; t0 < T; t0 += 32) {
-    const int t = t0 + lane;
-    const uint16_t *kr = nullptr, *vr = nullptr;
-    if (t < T) {
-      int64_t slot = p.seg_start[b] + t;
-      if (p.pages.table) {
-        const int32_t id = p.pages.table[(int64_t)b * p.pages.max_blocks + (t >> p.pages.shift)];
-        if (id < 0 || id >= p.pages.n_blocks) dev::set_error(p.err, TRIA_DEVERR_PAGES);
-        slot = ((int64_t)min(max(id, 0), p.pages.n_blocks - 1) << p.pages.shift) +
-               (t & ((1 << p.pages.shift) - 1));
+  *reinterpret_cast<volatile int32_t *>(&c.abort) = 1;
+  dev::set_error(err, TRIA_DEVERR_TIMEOUT);
+  return false;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int32_t x, int32_t y,
+                                            int32_t z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dev::smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(dev::smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The tiles [k0, k1) of unit (b, g, mg), which has K tiles, KT of them cached.
+struct Piece {
+  int b, g, mg, k0, k1, K, KT, T, n;
+};
+
+// Walks a CTA's share of the tile list, a piece at a time.
+template <int MT>
+struct Walk {
+  const TreeAttnParams &p;
+  const TreeCtl &c;
+  int b, g, mg, kt, left;
+
+  __device__ __forceinline__ int length(int b_, int g_) const {
+    if (!p.unit_len) return (int)(c.tn[b_] >> 9);
+    const int32_t t = p.unit_len[((int64_t)p.layer * p.Hkv + g_) * p.B + b_];
+    return t < 0 || (int64_t)t > p.seg_start[b_ + 1] - p.seg_start[b_] ? -1 : t;
+  }
+  __device__ __forceinline__ int nodes(int b_) const { return (int)(c.tn[b_] & 511u); }
+  // M groups of sequence b, and key tiles of a unit with T cached tokens (none if T < 0)
+  __device__ __forceinline__ int groups(int b_) const {
+    return (nodes(b_) * p.G + MT * kTile - 1) / (MT * kTile);
+  }
+  __device__ __forceinline__ int tiles(int b_, int T) const {
+    return T < 0 ? 0 : (T + kTile - 1) / kTile + (nodes(b_) + kTile - 1) / kTile;
+  }
+  __device__ __forceinline__ Walk(const TreeAttnParams &p_, const TreeCtl &c_, int left_)
+      : p(p_), c(c_), b(c_.start_b), g(0), mg(0), kt(0), left(left_) {
+    if (left <= 0) return;
+    int rem = c.start_rem;
+    const int M = groups(b);
+    for (g = 0; g < p.Hkv; ++g) {
+      const int K = tiles(b, length(b, g));
+      if (rem < K * M) {
+        mg = rem / K;
+        kt = rem - mg * K;
+        break;
       }
-      kr = p.k + (lg * p.cap + slot) * D;
-      vr = p.v + (lg * p.cap + slot) * D;
+      rem -= K * M;
     }
-    take(kr, vr);
   }
-  for (int j0 = 0; j0 <= i; j0 += 32) {
-    // the path's nodes of this group of 32
-    bool seen = false;
-    for (int j = i; j >= j0;) {
-      if (j == j0 + lane) seen = true;
-      const int32_t up = p.parent[(int64_t)b * p.N + j];
-      const bool fine = up >= -1 && up < j;
-      if (!fine) dev::set_error(p.err, TRIA_DEVERR_TREE);
-      j = fine ? up : -1;
+  __device__ __forceinline__ bool next(Piece &x) {
+    while (left > 0) {
+      if (g == p.Hkv || nodes(b) == 0) {
+        g = 0;
+        ++b;
+        continue;
+      }
+      const int T = length(b, g), K = tiles(b, T);
+      if (K == 0) {
+        ++g;
+        continue;
+      }
+      x.b = b;
+      x.g = g;
+      x.mg = mg;
+      x.k0 = kt;
+      x.k1 = min(K, kt + left);
+      x.K = K;
+      x.KT = (T + kTile - 1) / kTile;
+      x.T = T;
+      x.n = nodes(b);
+      left -= x.k1 - x.k0;
+      kt = 0;
+      if (++mg == groups(b)) {
+        mg = 0;
+        ++g;
+      }
+      return true;
     }
-    const int64_t node = (lg * p.B + b) * p.N + j0 + lane;
-    take(seen ? p.kd + node * D : nullptr, seen ? p.vd + node * D : nullptr);
+    return false;
   }
+};
+
+// Where tile x of a CTA's X tiles stands in the ring's order of K and V tiles.
+template <int MT>
+__device__ __forceinline__ int k_seq(int x) {
+  return MT == 2 ? 2 * x : x == 0 ? 0 : 2 * x - 1;  // MT = 1: K0 K1 V0 K2 V1 ...
+}
+template <int MT>
+__device__ __forceinline__ int v_seq(int x, int X) {
+  return MT == 2 ? 2 * x + 1 : x < X - 1 ? 2 * x + 2 : 2 * x + 1;
+}
+
+__device__ __forceinline__ int64_t share_start(int64_t total, int c, int ctas) {
+  return total * c / ctas;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
+    tree_attention_kernel(const __grid_constant__ TreeAttnParams p) {
+  using S = TreeShape<D, MT>;
+  constexpr int TB = S::TB, SLAB = S::SLAB, NS = S::NS, QB = S::QB, NB = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
+  TreeCtl &c = *reinterpret_cast<TreeCtl *>(sm + S::OFF_CTL);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+
+  // ---------------------------------------------------------------- setup
+  if (tid == 0) {
+    dev::pdl_launch_dependents();
+    p.desc[cta].b = -1;
+  }
+  int tiles_b = 0;
+  if (tid < TRIA_MAX_BATCH) {
+    int T = 0, n = 0;
+    if (tid < p.B) {
+      n = p.n_nodes[tid];
+      int bad = 0;
+      if (n < 0 || n > p.N) {
+        bad = TRIA_DEVERR_TREE;
+        n = 0;
+      }
+      const int64_t cap_b = p.seg_start[tid + 1] - p.seg_start[tid];
+      const int M = (n * p.G + MT * kTile - 1) / (MT * kTile), DT = (n + kTile - 1) / kTile;
+      if (p.unit_len) {
+        for (int g = 0; g < p.Hkv; ++g) {
+          const int32_t t = p.unit_len[((int64_t)p.layer * p.Hkv + g) * p.B + tid];
+          if (t < 0 || (int64_t)t > cap_b) bad |= TRIA_DEVERR_SEQ_LEN;
+          else tiles_b += M * ((t + kTile - 1) / kTile + DT);
+        }
+      } else {
+        T = p.seq_len[tid];
+        if (T < 0 || (int64_t)T > cap_b) {
+          bad |= TRIA_DEVERR_SEQ_LEN;
+          n = T = 0;
+        } else {
+          tiles_b = M * p.Hkv * ((T + kTile - 1) / kTile + DT);
+        }
+      }
+      if (bad && cta == 0) dev::set_error(p.err, bad);
+      c.tn[tid] = (uint32_t)T << 9 | (uint32_t)n;
+    }
+  }
+  if (warp == 1) tc::tmem_alloc<512>(&c.tmem);
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      dev::mbar_init(&c.full[i], 1);
+      dev::mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      dev::mbar_init(&c.q_full[i], 1);
+      dev::mbar_init(&c.q_empty[i], 1);
+      dev::mbar_init(&c.s_full[i], 1);
+      dev::mbar_init(&c.p_full[i], 128);
+      dev::mbar_init(&c.o_full[i], 1);
+      dev::mbar_init(&c.o_free[i], 128);
+    }
+    dev::mbar_init(&c.done, 1);
+    dev::fence_mbar_init();
+    c.abort = 0;
+  }
+  // prefix sums of the sequences' tiles
+  int incl = tiles_b;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out[row * D + lane + 32 * e] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] / l));
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (warp < 8 && lane == 31) c.warp_sums[warp] = incl;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  int64_t total = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) incl += c.warp_sums[w];
+    total += c.warp_sums[w];
+  }
+  // no share is empty but those of the last CTAs, where there are fewer tiles than CTAs
+  const int ctas = (int)min((int64_t)gridDim.x, total);
+  const int w0 = cta < ctas ? (int)share_start(total, cta, ctas) : 0;
+  const int w1 = cta < ctas ? (int)share_start(total, cta + 1, ctas) : 0;
+  const int X = w1 - w0;
+  if (X > 0 && tid < TRIA_MAX_BATCH && w0 >= incl - tiles_b && w0 < incl) {
+    c.start_b = tid;
+    c.start_rem = w0 - (incl - tiles_b);
+  }
+  __syncthreads();
+  const uint32_t tmem = c.tmem;
+  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + (MT == 2 ? D : 0)};
+
+  if (X > 0) {
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    Walk<MT> walk(p, c, X);
+    Piece u;
+    int x = 0, pi = 0;
+    // a tile's K or V rows into ring place `seq`
+    auto load = [&](const Piece &q, int kt, bool v, int seq, int32_t id) {
+      const int s = seq % NS, use = seq / NS;
+      if (use > 0) tree_wait(c, &c.empty[s], (use - 1) & 1, p.err);
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&c.abort))) return;
+      uint8_t *to = sm + S::OFF_RING + s * TB;
+      const int lg = p.layer * p.Hkv + q.g;
+      if (kt >= q.KT) {  // drafted nodes
+        if (lane == 0) {
+          dev::mbar_arrive_expect_tx(&c.full[s], (uint32_t)(NB * p.draft_rows * 128));
+          for (int cb = 0; cb < NB; ++cb)
+            tma_load_3d(to + cb * SLAB, v ? &p.tvd : &p.tkd, cb * 64, (kt - q.KT) * kTile,
+                        lg * p.B + q.b, &c.full[s]);
+        }
+      } else if (!p.pages.table) {
+        if (lane == 0) {
+          dev::mbar_arrive_expect_tx(&c.full[s], (uint32_t)TB);
+          for (int cb = 0; cb < NB; ++cb)
+            tma_load_3d(to + cb * SLAB, v ? &p.tv : &p.tk, cb * 64,
+                        (int32_t)p.seg_start[q.b] + kt * kTile, lg, &c.full[s]);
+        }
+      } else {
+        // lane j takes block j of the tile (blocks of 256: its half)
+        const int rows = min(kTile, 1 << p.pages.shift);
+        const int need = (min(kTile, q.T - kt * kTile) + rows - 1) / rows;
+        if (lane == 0) dev::mbar_arrive_expect_tx(&c.full[s], (uint32_t)(NB * need * rows * 128));
+        __syncwarp();
+        if (lane < need) {
+          const int32_t slot = (id << p.pages.shift) + (kt * kTile & ((1 << p.pages.shift) - 1) & ~(rows - 1));
+          for (int cb = 0; cb < NB; ++cb)
+            tma_load_3d(to + cb * SLAB + lane * rows * 128, v ? &p.tv : &p.tk, cb * 64, slot, lg,
+                        &c.full[s]);
+        }
+      }
+    };
+    // block id of lane j's rows in cached tile kt
+    auto block_of = [&](const Piece &q, int kt) -> int32_t {
+      if (!p.pages.table || kt >= q.KT) return 0;
+      const int rows = min(kTile, 1 << p.pages.shift);
+      const int t = kt * kTile + lane * rows;
+      if (lane * rows >= kTile || t >= q.T) return 0;
+      const int32_t id = p.pages.table[(int64_t)q.b * p.pages.max_blocks + (t >> p.pages.shift)];
+      if (id < 0 || id >= p.pages.n_blocks) {
+        dev::set_error(p.err, TRIA_DEVERR_PAGES);
+        return 0;
+      }
+      return id;
+    };
+    // the V of a tile follows the next tile's K (MT = 1), which may be another unit's
+    Piece vu = {};
+    int vkt = -1, vx = 0;
+    int32_t vid = 0;
+    while (walk.next(u)) {
+      const int qb = pi % QB, quse = pi / QB;
+      if (quse > 0) tree_wait(c, &c.q_empty[qb], (quse - 1) & 1, p.err);
+      if (lane == 0 && !*reinterpret_cast<volatile int32_t *>(&c.abort)) {
+        dev::mbar_arrive_expect_tx(&c.q_full[qb], (uint32_t)(MT * TB));
+        for (int m = 0; m < MT; ++m)
+          for (int cb = 0; cb < NB; ++cb)
+            tma_load_3d(sm + S::OFF_Q + (qb * MT + m) * TB + cb * SLAB, &p.tq, cb * 64, u.g * p.G,
+                        u.b * p.N + (u.mg * MT + m) * (kTile / p.G), &c.q_full[qb]);
+      }
+      __syncwarp();
+      for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
+        const int32_t id = block_of(u, kt);
+        load(u, kt, false, k_seq<MT>(x), id);
+        if (MT == 2) {
+          load(u, kt, true, v_seq<MT>(x, X), id);
+        } else {
+          if (x > 0) load(vu, vkt, true, v_seq<MT>(vx, X), vid);
+          vu = u;
+          vkt = kt;
+          vx = x;
+          vid = id;
+        }
+      }
+      ++pi;
+    }
+    if (MT == 1) load(vu, vkt, true, v_seq<MT>(vx, X), vid);
+    if (*reinterpret_cast<volatile int32_t *>(&c.abort)) {
+      // copies in flight land before the shared memory is given up
+      for (int i = 0; i < NS; ++i)
+        for (int k = 0; k < 2000 && !dev::mbar_try_wait(&c.full[i], 0) && !dev::mbar_try_wait(&c.full[i], 1); ++k) {
+        }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      Walk<MT> walk(p, c, X), ahead(p, c, X);
+      Piece u, ua;
+      int ka = 0, pa = -1;       // the next S product's tile and piece
+      bool more = ahead.next(ua);
+      if (more) {
+        ka = ua.k0;
+        pa = 0;
+      }
+      auto aborted = [&]() { return *reinterpret_cast<volatile int32_t *>(&c.abort) != 0; };
+      // S of tile x, M tile m
+      auto scores = [&](int x, int m, bool first, bool last) {
+        const int qb = pa % QB;
+        if (first) tree_wait(c, &c.q_full[qb], (pa / QB) & 1, p.err);
+        const int seq = k_seq<MT>(x), s = seq % NS;
+        if (m == 0) tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
+        if (aborted()) return;
+        tc::fence_after();
+        const int buf = MT == 2 ? m : x & 1;
+        const uint32_t qa = dev::smem_addr(sm + S::OFF_Q + (qb * MT + m) * TB);
+        const uint32_t ka_ = dev::smem_addr(sm + S::OFF_RING + s * TB);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (uint32_t)(k >> 2) * SLAB + (uint32_t)(k & 3) * 32;
+          tc::mma_ss(tm_s[buf], tc::desc(qa + off, 16), tc::desc(ka_ + off, 16),
+                     tc::instr(kTile, false), k > 0);
+        }
+        tc::commit(&c.s_full[buf]);
+        if (m == MT - 1) {
+          tc::commit(&c.empty[s]);
+          if (last) tc::commit(&c.q_empty[qb]);
+        }
+      };
+      // O of tile x, M tile m
+      auto output = [&](int x, int m, bool first, int pi) {
+        const int buf = MT == 2 ? m : x & 1;
+        tree_wait(c, &c.p_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
+        const int seq = v_seq<MT>(x, X), s = seq % NS;
+        if (m == 0) tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
+        if (first && pi > 0) tree_wait(c, &c.o_free[m], (pi - 1) & 1, p.err);
+        if (aborted()) return;
+        tc::fence_after();
+        const uint32_t va = dev::smem_addr(sm + S::OFF_RING + s * TB);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          tc::mma_ts(tm_o[m], tm_s[buf] + 8 * k, tc::desc(va + 2048 * k, SLAB), tc::instr(D, true),
+                     !first || k > 0);
+        tc::commit(&c.o_full[m]);
+        if (m == MT - 1) tc::commit(&c.empty[s]);
+      };
+      auto step_ahead = [&]() {
+        if (++ka == ua.k1) {
+          more = ahead.next(ua);
+          if (more) {
+            ka = ua.k0;
+            ++pa;
+          }
+        }
+      };
+      for (int m = 0; m < MT; ++m) scores(0, m, true, ka + 1 == ua.k1);
+      step_ahead();
+      int x = 0, pi = 0;
+      while (walk.next(u)) {
+        for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
+          for (int m = 0; m < MT; ++m) {
+            if (MT == 1 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
+            output(x, m, kt == u.k0, pi);
+            if (MT == 2 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
+          }
+          if (more) step_ahead();
+        }
+        ++pi;
+      }
+      if (aborted()) {  // products in flight complete before tensor memory is given up
+        tc::commit(&c.done);
+        for (int k = 0; k < 2000 && !dev::mbar_try_wait(&c.done, 0); ++k) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax
+    const int m = (warp - 4) >> 2, row = tid - 128 - 128 * m;  // row of M tile m
+    const uint32_t lane_off = (uint32_t)(warp & 3) << 21;      // 32 lanes of tensor memory
+    const float sl = p.scale * 1.4426950408889634f;            // logits in powers of two
+    const int per = kTile / p.G;                               // nodes per M tile
+    Walk<MT> walk(p, c, X);
+    Piece u;
+    int x = 0, o_seen = 0;
+    // The products with V up to that of tile x - 1 have completed.  Every tile awaits that
+    // before it hands over its own P (by then they have, as a rule): a barrier's parity tells
+    // only the last two phases apart, so none may be passed over or left behind.
+    auto outputs_before = [&](int x) {
+      for (; o_seen < x; ++o_seen) tree_wait(c, &c.o_full[m], o_seen & 1, p.err);
+      __syncwarp();
+    };
+    while (walk.next(u)) {
+      const int node0 = (u.mg * MT + m) * per;
+      const int node = node0 + row / p.G, head = u.g * p.G + row % p.G;
+      const bool live = node < u.n;
+      const bool any = node0 + (row & ~31) / p.G < u.n;  // the warp has a live row
+      const bool drafts = u.k1 > u.KT;
+      int16_t up0 = -1, up1 = -1;
+      if (drafts && m == 0) {  // the parents, ahead of their use
+        auto fetch = [&](int i) -> int16_t {
+          if (i >= u.n) return -1;
+          const int32_t v = p.parent[(int64_t)u.b * p.N + i];
+          if (v >= -1 && v < i) return (int16_t)v;
+          dev::set_error(p.err, TRIA_DEVERR_TREE);
+          return -1;
+        };
+        up0 = fetch(row);
+        up1 = fetch(row + 128);
+      }
+      float mr = -INFINITY, l = 0.0f;
+      uint32_t hurt[2][4] = {};  // nodes on this row's path whose V has Inf or NaN
+      for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
+        const int buf = MT == 2 ? m : x & 1;
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool draft = kt >= u.KT;
+        const int valid = draft ? u.n - (kt - u.KT) * kTile : u.T - kt * kTile;  // columns (may pass 128)
+        const bool masked = draft || valid < kTile;
+        if (masked) {
+          // this tile's V in shared memory: rows past `valid` become zero, and in a tile of
+          // nodes so do Inf and NaN
+          const int seq = v_seq<MT>(x, X), s = seq % NS;
+          // (a ring of two: the tile before in this place, the last V or this K, may still be
+          // on its way)
+          if (NS < 4) {
+            outputs_before(x);
+            tree_wait(c, &c.s_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
+          }
+          tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
+          uint8_t *vt = sm + S::OFF_RING + s * TB;
+          if (draft) {
+            constexpr int ALL = 128 * MT;
+            dev::named_barrier(1, ALL);  // the last tile's marks have been read
+            if (m == 0) {
+              if (row < 4) c.poison[row] = 0;
+              c.parent[row] = up0;
+              c.parent[row + 128] = up1;
+            }
+            dev::named_barrier(1, ALL);
+            for (int i = tid - 128; i < kTile * D / 8; i += ALL) {
+              uint4 *at = reinterpret_cast<uint4 *>(vt) + i;
+              const int r = (i >> 3) & (kTile - 1);
+              if (r >= valid) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+              }
+              uint4 w = *at;
+              uint32_t *ws = &w.x;
+              bool bad = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((ws[e] & 0x7f80u) == 0x7f80u) {
+                  ws[e] &= 0xffff0000u;
+                  bad = true;
+                }
+                if ((ws[e] & 0x7f800000u) == 0x7f800000u) {
+                  ws[e] &= 0x0000ffffu;
+                  bad = true;
+                }
+              }
+              if (bad) {
+                *at = w;
+                atomicOr(&c.poison[r >> 5], 1u << (r & 31));
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            dev::named_barrier(1, ALL);
+            // the columns on this row's path
+            const int j0 = (kt - u.KT) * kTile;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) seen[e] = 0u;
+            if (live)
+              for (int j = node; j >= j0; j = c.parent[j]) {
+                const int q = j - j0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if ((q >> 5) == e) seen[e] |= 1u << (q & 31);
+              }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j0) hurt[1][e] = seen[e] & c.poison[e];
+              else hurt[0][e] = seen[e] & c.poison[e];
+          } else {
+            for (int i = tid - 128 - 128 * m; i < (kTile - valid) * (D / 8); i += 128) {
+              const int r = valid + i / (D / 8), q = i % (D / 8);
+              *(reinterpret_cast<uint4 *>(vt + (q >> 3) * SLAB + r * 128) + (q & 7)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              seen[e] = valid >= 32 * (e + 1) ? ~0u : valid <= 32 * e ? 0u : (1u << (valid - 32 * e)) - 1u;
+          }
+        }
+        tree_wait(c, &c.s_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
+        __syncwarp();
+        tc::fence_after();
+        if (any) {
+          float s[kTile];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            tc::ld32(tm_s[buf] + lane_off + 32 * e, reinterpret_cast<uint32_t *>(s) + 32 * e);
+          tc::wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(seen[e] >> i & 1u)) s[32 * e + i] = -INFINITY;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < kTile; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[i + e]);
+          const float mn = fmaxf(mr, sl * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (__any_sync(0xffffffffu, mn > mr + 8.0f)) {
+            const float a = mr == -INFINITY ? 0.0f : exp2_approx(mr - mn);
+            if (kt > u.k0) {
+              outputs_before(x);
+              tc::fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                uint32_t o[32];
+                tc::ld32(tm_o[m] + lane_off + d, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                tc::st32(tm_o[m] + lane_off + d, o);
+              }
+            }
+            l *= a;
+            mr = mn;
+          }
+          const float base = mr == -INFINITY ? 0.0f : mr;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float a0 = exp2_approx(fmaf(s[64 * e + 2 * i], sl, -base));
+              const float a1 = exp2_approx(fmaf(s[64 * e + 2 * i + 1], sl, -base));
+              sum[(2 * i) & 3] += a0;
+              sum[(2 * i + 1) & 3] += a1;
+              w[i] = pack_bf16x2(a0, a1);
+            }
+            tc::st32(tm_s[buf] + lane_off + 32 * e, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc::wait_st();
+        }
+        outputs_before(x);
+        tc::fence_before();
+        dev::mbar_arrive(&c.p_full[buf]);
+      }
+      // ------------------------------------------------------------ the unit, or its part
+      outputs_before(x);
+      tc::fence_after();
+      const bool whole = u.k0 == 0 && u.k1 == u.K;
+      float *part = p.scratch + ((size_t)cta * kPartSlots + (u.k0 > 0 ? 0 : 1)) * (size_t)(MT * kTile) * (D + 2);
+      const int r = m * kTile + row;
+      if (any) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint4 *to = reinterpret_cast<uint4 *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D);
+        bool any_hurt = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any_hurt |= (hurt[0][e] | hurt[1][e]) != 0;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          float o[32];
+          __syncwarp();
+          tc::ld32(tm_o[m] + lane_off + d, reinterpret_cast<uint32_t *>(o));
+          tc::wait_ld();
+          if (any_hurt) {
+            for (int e = 0; e < 8; ++e)
+              for (uint32_t bits = hurt[e >> 2][e & 3]; bits; bits &= bits - 1) {
+                const int j = 32 * e + __ffs(bits) - 1;
+                const uint16_t *v = p.vd + ((((int64_t)p.layer * p.Hkv + u.g) * p.B + u.b) * p.N + j) * D + d;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float f = __uint_as_float((uint32_t)v[i] << 16);
+                  if (!isfinite(f)) o[i] += f;
+                }
+              }
+          }
+          if (live && whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              to[(d + i) / 8] = make_uint4(pack_bf16x2(o[i] * inv, o[i + 1] * inv),
+                                           pack_bf16x2(o[i + 2] * inv, o[i + 3] * inv),
+                                           pack_bf16x2(o[i + 4] * inv, o[i + 5] * inv),
+                                           pack_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
+          } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) part[(size_t)(d + i) * (MT * kTile) + r] = o[i];
+          }
+        }
+        if (!whole && live) {
+          part[(size_t)D * (MT * kTile) + r] = mr;
+          part[(size_t)(D + 1) * (MT * kTile) + r] = l;
+        }
+      }
+      tc::fence_before();
+      dev::mbar_arrive(&c.o_free[m]);
+      // the unit goes on in the next CTAs: what the merge needs to know
+      if (m == 0 && row == 0 && u.k0 == 0 && u.k1 < u.K) {
+        const int64_t end = (int64_t)w0 + x - (u.k1 - u.k0) + u.K;  // past the unit's last tile
+        TreeDesc d = {u.b, u.g, u.mg, u.n, (int32_t)((end * ctas + total - 1) / total) - 1};
+        p.desc[cta] = d;
+      }
+    }
+  }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 1) tc::tmem_free<512>(tmem);
+}
+
+// Merges the parts of the units that more than one CTA worked on: block (c, m, e) takes M tile
+// m and 32 output dims of the unit that CTA c's share ends in.
+template <int D, int MT>
+__global__ void __launch_bounds__(kTile) tree_merge_kernel(const __grid_constant__ TreeAttnParams p) {
+  dev::pdl_wait();
+  const int c0 = blockIdx.x;
+  const TreeDesc u = p.desc[c0];
+  if (u.b < 0) return;
+  const int m = blockIdx.y, row = threadIdx.x, d0 = blockIdx.z * 32, r = m * kTile + row;
+  const int node = (u.mg * MT + m) * (kTile / p.G) + row / p.G, head = u.g * p.G + row % p.G;
+  if (node >= u.n) return;
+  constexpr size_t PART = (size_t)(MT * kTile) * (D + 2);
+  auto part = [&](int ct) { return p.scratch + ((size_t)ct * kPartSlots + (ct == c0 ? 1 : 0)) * PART + r; };
+  float M = -INFINITY;
+  for (int ct = c0; ct <= u.last; ++ct) M = fmaxf(M, __ldcg(part(ct) + (size_t)D * (MT * kTile)));
+  if (M == -INFINITY) M = 0.0f;
+  float L = 0.0f, o[32] = {};
+  for (int ct = c0; ct <= u.last; ++ct) {
+    const float *x = part(ct);
+    const float mc = __ldcg(x + (size_t)D * (MT * kTile)), l = __ldcg(x + (size_t)(D + 1) * (MT * kTile));
+    // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
+    const float w = mc == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc - M);
+    L = fmaf(w, l, L);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = fmaf(w, __ldcg(x + (size_t)(d0 + i) * (MT * kTile)), o[i]);
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint4 *to = reinterpret_cast<uint4 *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D + d0);
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    to[i / 8] = make_uint4(pack_bf16x2(o[i] * inv, o[i + 1] * inv), pack_bf16x2(o[i + 2] * inv, o[i + 3] * inv),
+                           pack_bf16x2(o[i + 4] * inv, o[i + 5] * inv), pack_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, []() {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return encode;
+}
+
+// bf16 [z][y][D], boxes of 64 columns x by x bz.
+bool map_3d(CUtensorMap *map, const void *base, int D, int64_t y, int64_t z, int by, int bz) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * (cuuint64_t)y};
+  const cuuint32_t box[3] = {64, (cuuint32_t)by, (cuuint32_t)bz};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// M tiles per unit: two as soon as one does not hold the tree's rows (K and V are then read
+// once for 256 rows), but for D = 256, whose accumulator fills tensor memory.
+int m_tiles(int D, int G, int N) { return D < 256 && N * G > kTile ? 2 : 1; }
+
+size_t desc_bytes() { return ((size_t)device_sm_count() * sizeof(TreeDesc) + 255) / 256 * 256; }
+
+template <int D, int MT>
+cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
+  auto kern = tree_attention_kernel<D, MT>;
+  constexpr int smem = tree_smem<D, MT>();
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static bool set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  kern<<<ctas, TreeShape<D, MT>::THREADS, smem, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, MT, D / 32);
+  cfg.blockDim = dim3(kTile, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, MT>, p);
 }
 
 }  // namespace
 
 size_t tree_attention_scratch(int D, int G, int N) {
-  (void)D;
-  (void)G;
-  (void)N;
-  return 0;
+  return desc_bytes() +
+         (size_t)device_sm_count() * kPartSlots * (size_t)(m_tiles(D, G, N) * kTile) * (D + 2) * sizeof(float);
 }
 
-cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t s) {
-  const int64_t blocks = ((int64_t)p.B * p.N * p.Hq + kRowWarps - 1) / kRowWarps;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  switch (p.D) {
-    case 64: tree_rows_kernel<64><<<(unsigned)blocks, kRowWarps * 32, 0, s>>>(p); break;
-    case 128: tree_rows_kernel<128><<<(unsigned)blocks, kRowWarps * 32, 0, s>>>(p); break;
-    case 256: tree_rows_kernel<256><<<(unsigned)blocks, kRowWarps * 32, 0, s>>>(p); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+cudaError_t launch_tree_attention(const TreeAttnParams &params, void *scratch, cudaStream_t s) {
+  TreeAttnParams p = params;
+  p.desc = static_cast<TreeDesc *>(scratch);
+  p.scratch = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + desc_bytes());
+  const int mt = m_tiles(p.D, p.G, p.N);
+  // the most tiles that there can be: all segments full
+  int64_t most = 0;
+  for (int b = 0; b < p.B; ++b)
+    most += (p.seg_start[b + 1] - p.seg_start[b] + kTile - 1) / kTile + (p.N + kTile - 1) / kTile;
+  most *= (int64_t)p.Hkv * ((p.N * p.G + mt * kTile - 1) / (mt * kTile));
+  const int64_t heads = (int64_t)p.L * p.Hkv;
+  if (most > INT32_MAX || p.cap > INT32_MAX || heads * p.B > INT32_MAX) return cudaErrorInvalidValue;
+  p.draft_rows = p.N < kTile ? p.N : kTile;
+  const int rows = p.pages.table && p.pages.shift < 7 ? 1 << p.pages.shift : kTile;
+  if (!map_3d(&p.tk, p.k, p.D, p.cap, heads, rows, 1) || !map_3d(&p.tv, p.v, p.D, p.cap, heads, rows, 1) ||
+      !map_3d(&p.tkd, p.kd, p.D, p.N, heads * p.B, p.draft_rows, 1) ||
+      !map_3d(&p.tvd, p.vd, p.D, p.N, heads * p.B, p.draft_rows, 1) ||
+      !map_3d(&p.tq, p.q, p.D, p.Hq, (int64_t)p.B * p.N, p.G, kTile / p.G))
+    return cudaErrorInvalidValue;
+  const int sms = device_sm_count(), ctas = (int)(most < sms ? most : sms);
+  if (p.D == 64) return mt == 2 ? launch<64, 2>(p, ctas, s) : launch<64, 1>(p, ctas, s);
+  if (p.D == 128) return mt == 2 ? launch<128, 2>(p, ctas, s) : launch<128, 1>(p, ctas, s);
+  return launch<256, 1>(p, ctas, s);
 }
 
 }  // namespace tria

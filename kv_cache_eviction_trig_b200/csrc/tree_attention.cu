@@ -705,38 +705,73 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   if (warp == 1) tc::tmem_free<512>(tmem);
 }
 
-// Merges the parts of the units that more than one CTA worked on: block (c, m, e) takes M tile
-// m and 32 output dims of the unit that CTA c's share ends in.
+// Merges the parts of the units that more than one CTA worked on: block (c, y, e) takes 32
+// rows and kMergeDims output dims of the unit that CTA c's share ends in.  Lane = row; warp w
+// adds up the parts w, w + 8, ... (a serial pass over the parts is bound by the latency of
+// its loads), and the warps' sums meet in shared memory, in the order of the warps.
+constexpr int kMergeDims = 64, kMergeWarps = 8;
+
 template <int D, int MT>
-__global__ void __launch_bounds__(kTile) tree_merge_kernel(const __grid_constant__ TreeAttnParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    tree_merge_kernel(const __grid_constant__ TreeAttnParams p) {
+  constexpr int ROWS = MT * kTile, DC = 16;  // dims per pass
+  constexpr size_t PART = (size_t)ROWS * (D + 2);
+  __shared__ float sm_o[kMergeWarps][DC][33], sm_l[kMergeWarps][32], sm_m[kMergeWarps][32];
   dev::pdl_wait();
   const int c0 = blockIdx.x;
   const TreeDesc u = p.desc[c0];
   if (u.b < 0) return;
-  const int m = blockIdx.y, row = threadIdx.x, d0 = blockIdx.z * 32, r = m * kTile + row;
-  const int node = (u.mg * MT + m) * (kTile / p.G) + row / p.G, head = u.g * p.G + row % p.G;
-  if (node >= u.n) return;
-  constexpr size_t PART = (size_t)(MT * kTile) * (D + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = kTile / p.G;
+  // row r of the unit: node, head; rows past the nodes read a part's other rows and write nothing
+  const int r = blockIdx.y * 32 + lane;
+  const int node = u.mg * MT * per + r / p.G, head = u.g * p.G + r % p.G;
+  if (u.mg * MT * per + (int)blockIdx.y * 32 / p.G >= u.n) return;
+  const bool live = node < u.n;
   auto part = [&](int ct) { return p.scratch + ((size_t)ct * kPartSlots + (ct == c0 ? 1 : 0)) * PART + r; };
   float M = -INFINITY;
-  for (int ct = c0; ct <= u.last; ++ct) M = fmaxf(M, __ldcg(part(ct) + (size_t)D * (MT * kTile)));
+  if (live)
+    for (int ct = c0 + warp; ct <= u.last; ct += kMergeWarps) M = fmaxf(M, part(ct)[(size_t)D * ROWS]);
+  sm_m[warp][lane] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, sm_m[w][lane]);
   if (M == -INFINITY) M = 0.0f;
-  float L = 0.0f, o[32] = {};
-  for (int ct = c0; ct <= u.last; ++ct) {
-    const float *x = part(ct);
-    const float mc = __ldcg(x + (size_t)D * (MT * kTile)), l = __ldcg(x + (size_t)(D + 1) * (MT * kTile));
-    // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
-    const float w = mc == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc - M);
-    L = fmaf(w, l, L);
+#pragma unroll 1
+  for (int d0 = blockIdx.z * kMergeDims; d0 < (int)(blockIdx.z + 1) * kMergeDims; d0 += DC) {
+    float L = 0.0f, o[DC] = {};
+    if (live)
+      for (int ct = c0 + warp; ct <= u.last; ct += kMergeWarps) {
+        const float *x = part(ct);
+        float v[DC];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = fmaf(w, __ldcg(x + (size_t)(d0 + i) * (MT * kTile)), o[i]);
+        for (int i = 0; i < DC; ++i) v[i] = x[(size_t)(d0 + i) * ROWS];
+        const float mc = x[(size_t)D * ROWS], l = x[(size_t)(D + 1) * ROWS];
+        // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
+        const float w = mc == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc - M);
+        L = fmaf(w, l, L);
+#pragma unroll
+        for (int i = 0; i < DC; ++i) o[i] = fmaf(w, v[i], o[i]);
+      }
+    __syncthreads();  // the last pass has been read
+    sm_l[warp][lane] = L;
+#pragma unroll
+    for (int i = 0; i < DC; ++i) sm_o[warp][i][lane] = o[i];
+    __syncthreads();
+    // thread (row, dim pair)
+    L = 0.0f;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      L += sm_l[w][lane];
+      a += sm_o[w][2 * warp][lane];
+      b += sm_o[w][2 * warp + 1][lane];
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    if (live)
+      reinterpret_cast<uint32_t *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D + d0)[warp] =
+          pack_bf16x2(a * inv, b * inv);
   }
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  uint4 *to = reinterpret_cast<uint4 *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D + d0);
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    to[i / 8] = make_uint4(pack_bf16x2(o[i] * inv, o[i + 1] * inv), pack_bf16x2(o[i + 2] * inv, o[i + 3] * inv),
-                           pack_bf16x2(o[i + 4] * inv, o[i + 5] * inv), pack_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -788,8 +823,9 @@ cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, MT, D / 32);
-  cfg.blockDim = dim3(kTile, 1, 1);
+  const int rows = min(p.N * p.G, MT * kTile);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(rows + 31) / 32, D / kMergeDims);
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -48,17 +48,17 @@ struct TreeCommitParams {
 };
 cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t s);
 
-// What a CTA of the attention leaves for the merge: the unit that its share of the tiles
-// ends in, if that goes on in the next CTAs.
+// A unit of the attention (sequence, KV head, group of M tiles) whose key tiles lie in more
+// than one CTA's share, for the merge.
 struct alignas(32) TreeDesc {
-  int32_t b, g, mg, n, last;  // b < 0: none; last: the CTA where the unit ends
+  int32_t b, g, mg, n, first, last;  // b < 0: none; n: its nodes; the CTAs that it starts and ends in
 };
 
 struct alignas(64) TreeAttnParams {
   CUtensorMap tk, tv;       // K and V as [L*Hkv][cap][D], boxes of 64 columns x 128 rows (or a block)
   CUtensorMap tkd, tvd;     // the nodes' as [L*Hkv*B][N][D], boxes of 64 x draft_rows
   CUtensorMap tq;           // the queries as [B*N][Hq][D], boxes of 64 x G heads x 128 / G nodes
-  TreeDesc *desc;           // one per CTA
+  TreeDesc *desc;           // one per unit (by_unit of them) or, if that is 0, per CTA
   float *scratch;           // two parts per CTA: unnormalised output [D][rows], maxima, sums
   const int32_t *parent;    // [B][N]
   const int32_t *n_nodes;   // [B]
@@ -73,7 +73,7 @@ struct alignas(64) TreeAttnParams {
   int32_t *err;
   PageParams pages;
   int64_t cap;
-  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows;
+  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows, by_unit, merge_dims;
   float scale;
   int64_t seg_start[TRIA_MAX_BATCH + 1];
 };

@@ -14,8 +14,9 @@
 //                 a box per block of a paged cache), and the units' queries;
 //   warp 1        one thread issues the tensor products: S = Q K^T into tensor memory, and
 //                 O += P V with P read from tensor memory, where it overlays S;
-//   warps 4..     a warpgroup per M tile, a thread per row: S from tensor memory, the
-//                 running maximum and sum, P = 2^(S - m) as bf16 back to tensor memory.
+//   warps 4..     two warpgroups per M tile, a thread per row and half of the tile's keys: S
+//                 from tensor memory, the running maximum (the two threads of a row exchange
+//                 theirs) and sum, P = 2^(S - m) as bf16 back to tensor memory.
 // The next tile's S is computed while this one's softmax runs (MT = 1: two S buffers; MT = 2:
 // the M tiles alternate).  O stays in tensor memory and is rescaled only when a row's
 // maximum grew by more than 2^8 (P is at most 2^8 then; float32 sums lose nothing).
@@ -35,6 +36,8 @@
 // What bounds it: K and V bytes for up to about 256 rows per KV head, the products above.
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <algorithm>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -42,6 +45,10 @@
 #include "mma_sync.cuh"
 #include "tcgen05.cuh"
 #include "tree.cuh"
+
+#ifndef TREE_NH2
+#define TREE_NH2 1
+#endif
 
 namespace tria {
 
@@ -54,12 +61,13 @@ template <int D, int MT>
 struct TreeShape {
   static constexpr int TB = kTile * D * 2;               // a K or V tile, or an M tile of queries
   static constexpr int SLAB = kTile * 128;               // 128 rows of 64 columns
-  static constexpr int QB = D == 256 || (D == 128 && MT == 2) ? 1 : 2;  // query buffers
+  static constexpr int QB = D == 64 ? 2 : 1;              // query buffers
   static constexpr int NS = D == 256 ? 2 : D == 64 ? 8 : MT == 2 ? 4 : 5;  // ring slots
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = QB * MT * TB;
   static constexpr int OFF_CTL = OFF_RING + NS * TB;
-  static constexpr int THREADS = 128 + 128 * MT;
+  static constexpr int NH = MT == 2 ? TREE_NH2 : 2;      // threads per row
+  static constexpr int THREADS = 128 + 128 * NH * MT;
 };
 
 struct TreeCtl {
@@ -69,6 +77,7 @@ struct TreeCtl {
   int32_t start_b, start_rem;          // where this CTA's share starts
   int32_t warp_sums[8];
   uint32_t poison[4];                  // drafted V rows of the tile with Inf or NaN
+  float swap[2][2][2][kTile];          // by tile parity, M tile and half: maxima, at the end sums
   uint32_t tn[TRIA_MAX_BATCH];         // live length (0 with per-unit lengths) << 9 | nodes (0: skipped)
   int16_t parent[TRIA_MAX_NODES];
 };
@@ -208,7 +217,9 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   // ---------------------------------------------------------------- setup
   if (tid == 0) {
     dev::pdl_launch_dependents();
-    p.desc[cta].b = -1;
+    const CUtensorMap *maps[] = {&p.tq, &p.tk, &p.tv, &p.tkd, &p.tvd};
+    for (const CUtensorMap *t : maps)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(t)) : "memory");
   }
   int tiles_b = 0;
   if (tid < TRIA_MAX_BATCH) {
@@ -251,9 +262,9 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       dev::mbar_init(&c.q_full[i], 1);
       dev::mbar_init(&c.q_empty[i], 1);
       dev::mbar_init(&c.s_full[i], 1);
-      dev::mbar_init(&c.p_full[i], 128);
+      dev::mbar_init(&c.p_full[i], 128 * S::NH);
       dev::mbar_init(&c.o_full[i], 1);
-      dev::mbar_init(&c.o_free[i], 128);
+      dev::mbar_init(&c.o_free[i], 128 * S::NH);
     }
     dev::mbar_init(&c.done, 1);
     dev::fence_mbar_init();
@@ -267,6 +278,21 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     if (lane >= o) incl += x;
   }
   if (warp < 8 && lane == 31) c.warp_sums[warp] = incl;
+  // the merge finds a unit that goes on in other CTAs by its number, or where there are more
+  // units than CTAs by the CTA that it starts in; the others' entries say that there is none
+  if (p.by_unit) {
+    if (cta == 0 && tid < p.by_unit) {
+      const int M = (p.N * p.G + MT * kTile - 1) / (MT * kTile);
+      const int mg = tid % M, b = tid / M / p.Hkv;
+      int32_t n = p.n_nodes[b];
+      if (n < 0 || n > p.N) n = 0;
+      const int32_t t = p.unit_len ? p.unit_len[((int64_t)p.layer * p.Hkv + tid / M % p.Hkv) * p.B + b] : p.seq_len[b];
+      if (mg * MT * kTile >= n * p.G || t < 0 || (int64_t)t > p.seg_start[b + 1] - p.seg_start[b])
+        p.desc[tid].b = -1;
+    }
+  } else if (tid == 0) {
+    p.desc[cta].b = -1;
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -381,92 +407,96 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      Walk<MT> walk(p, c, X), ahead(p, c, X);
-      Piece u, ua;
-      int ka = 0, pa = -1;       // the next S product's tile and piece
-      bool more = ahead.next(ua);
-      if (more) {
-        ka = ua.k0;
-        pa = 0;
-      }
-      auto aborted = [&]() { return *reinterpret_cast<volatile int32_t *>(&c.abort) != 0; };
-      // S of tile x, M tile m
-      auto scores = [&](int x, int m, bool first, bool last) {
-        const int qb = pa % QB;
-        if (first) tree_wait(c, &c.q_full[qb], (pa / QB) & 1, p.err);
-        const int seq = k_seq<MT>(x), s = seq % NS;
-        if (m == 0) tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
-        if (aborted()) return;
-        tc::fence_after();
-        const int buf = MT == 2 ? m : x & 1;
-        const uint32_t qa = dev::smem_addr(sm + S::OFF_Q + (qb * MT + m) * TB);
-        const uint32_t ka_ = dev::smem_addr(sm + S::OFF_RING + s * TB);
+    const uint32_t one = tc::elect_one();
+    Walk<MT> walk(p, c, X), ahead(p, c, X);
+    Piece u, ua;
+    int ka = 0, pa = -1;       // the next S product's tile and piece
+    bool more = ahead.next(ua);
+    if (more) {
+      ka = ua.k0;
+      pa = 0;
+    }
+    bool gone = false;         // a wait ran out: nothing is issued any more
+    auto await = [&](uint64_t *bar, int phase) {
+      if (!tree_wait(c, bar, phase & 1, p.err)) gone = true;
+    };
+    auto settled = [&]() {     // the warp is together again, and of one mind
+      gone = __any_sync(0xffffffffu, gone);
+      tc::fence_after();
+      return !gone;
+    };
+    const uint32_t base_lo = __shfl_sync(0xffffffffu, dev::smem_addr(sm), 0);
+    // S of tile x, M tile m
+    auto scores = [&](int x, int m, bool first, bool last) {
+      const int qb = pa % QB, seq = k_seq<MT>(x), s = seq % NS, buf = MT == 2 ? m : x & 1;
+      if (first) await(&c.q_full[qb], pa / QB);
+      if (m == 0) await(&c.full[s], seq / NS);
+      if (!settled()) return;
+      const uint64_t qd = tc::desc(base_lo + S::OFF_Q + (qb * MT + m) * TB, 16);
+      const uint64_t kd = tc::desc(base_lo + S::OFF_RING + s * TB, 16);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)(k >> 2) * SLAB + (uint32_t)(k & 3) * 32;
-          tc::mma_ss(tm_s[buf], tc::desc(qa + off, 16), tc::desc(ka_ + off, 16),
-                     tc::instr(kTile, false), k > 0);
-        }
-        tc::commit(&c.s_full[buf]);
-        if (m == MT - 1) {
-          tc::commit(&c.empty[s]);
-          if (last) tc::commit(&c.q_empty[qb]);
-        }
-      };
-      // O of tile x, M tile m
-      auto output = [&](int x, int m, bool first, int pi) {
-        const int buf = MT == 2 ? m : x & 1;
-        tree_wait(c, &c.p_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
-        const int seq = v_seq<MT>(x, X), s = seq % NS;
-        if (m == 0) tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
-        if (first && pi > 0) tree_wait(c, &c.o_free[m], (pi - 1) & 1, p.err);
-        if (aborted()) return;
-        tc::fence_after();
-        const uint32_t va = dev::smem_addr(sm + S::OFF_RING + s * TB);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc::mma_ts(tm_o[m], tm_s[buf] + 8 * k, tc::desc(va + 2048 * k, SLAB), tc::instr(D, true),
-                     !first || k > 0);
-        tc::commit(&c.o_full[m]);
-        if (m == MT - 1) tc::commit(&c.empty[s]);
-      };
-      auto step_ahead = [&]() {
-        if (++ka == ua.k1) {
-          more = ahead.next(ua);
-          if (more) {
-            ka = ua.k0;
-            ++pa;
-          }
-        }
-      };
-      for (int m = 0; m < MT; ++m) scores(0, m, true, ka + 1 == ua.k1);
-      step_ahead();
-      int x = 0, pi = 0;
-      while (walk.next(u)) {
-        for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
-          for (int m = 0; m < MT; ++m) {
-            if (MT == 1 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
-            output(x, m, kt == u.k0, pi);
-            if (MT == 2 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
-          }
-          if (more) step_ahead();
-        }
-        ++pi;
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((uint32_t)(k >> 2) * SLAB + (uint32_t)(k & 3) * 32) >> 4;
+        tc::mma_ss(tm_s[buf], qd + off, kd + off, tc::instr(kTile, false), k > 0, one);
       }
-      if (aborted()) {  // products in flight complete before tensor memory is given up
-        tc::commit(&c.done);
-        for (int k = 0; k < 2000 && !dev::mbar_try_wait(&c.done, 0); ++k) {
+      tc::commit(&c.s_full[buf], one);
+      if (m == MT - 1) {
+        tc::commit(&c.empty[s], one);
+        if (last) tc::commit(&c.q_empty[qb], one);
+      }
+    };
+    // O of tile x, M tile m
+    auto output = [&](int x, int m, bool first, int pi) {
+      const int seq = v_seq<MT>(x, X), s = seq % NS, buf = MT == 2 ? m : x & 1;
+      await(&c.p_full[buf], MT == 2 ? x : x >> 1);
+      if (m == 0) await(&c.full[s], seq / NS);
+      if (first && pi > 0) await(&c.o_free[m], pi - 1);
+      if (!settled()) return;
+      const uint64_t vd = tc::desc(base_lo + S::OFF_RING + s * TB, SLAB);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        tc::mma_ts(tm_o[m], tm_s[buf] + 8 * k, vd + (2048 >> 4) * k, tc::instr(D, true), !first || k > 0, one);
+      tc::commit(&c.o_full[m], one);
+      if (m == MT - 1) tc::commit(&c.empty[s], one);
+    };
+    auto step_ahead = [&]() {
+      if (++ka == ua.k1) {
+        more = ahead.next(ua);
+        if (more) {
+          ka = ua.k0;
+          ++pa;
         }
+      }
+    };
+    for (int m = 0; m < MT; ++m) scores(0, m, true, ka + 1 == ua.k1);
+    step_ahead();
+    int x = 0, pi = 0;
+    while (walk.next(u)) {
+      for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
+        for (int m = 0; m < MT; ++m) {
+          if (MT == 1 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
+          output(x, m, kt == u.k0, pi);
+          if (MT == 2 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
+        }
+        if (more) step_ahead();
+      }
+      ++pi;
+    }
+    if (gone) {  // products in flight complete before tensor memory is given up
+      tc::commit(&c.done, one);
+      for (int k = 0; k < 2000 && !dev::mbar_try_wait(&c.done, 0); ++k) {
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax
-    const int m = (warp - 4) >> 2, row = tid - 128 - 128 * m;  // row of M tile m
-    const uint32_t lane_off = (uint32_t)(warp & 3) << 21;      // 32 lanes of tensor memory
+    constexpr int NH = S::NH, HK = kTile / NH, HD = D / NH;    // keys and output dims per thread
+    const int q4 = warp & 3, m = (warp - 4) / (4 * NH), half = NH == 2 ? ((warp - 4) >> 2) & 1 : 0;
+    const int row = q4 * 32 + lane, part_id = half * 128 + row;  // row of M tile m; its thread
+    const uint32_t lane_off = (uint32_t)q4 << 21;              // 32 lanes of tensor memory
     const float sl = p.scale * 1.4426950408889634f;            // logits in powers of two
     const int per = kTile / p.G;                               // nodes per M tile
+    const uint32_t pair = 2 + m * 4 + q4;                      // barrier of a row's two warps (NH = 2)
     Walk<MT> walk(p, c, X);
     Piece u;
     int x = 0, o_seen = 0;
@@ -482,24 +512,22 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       const int node = node0 + row / p.G, head = u.g * p.G + row % p.G;
       const bool live = node < u.n;
       const bool any = node0 + (row & ~31) / p.G < u.n;  // the warp has a live row
-      const bool drafts = u.k1 > u.KT;
-      int16_t up0 = -1, up1 = -1;
-      if (drafts && m == 0) {  // the parents, ahead of their use
-        auto fetch = [&](int i) -> int16_t {
-          if (i >= u.n) return -1;
-          const int32_t v = p.parent[(int64_t)u.b * p.N + i];
-          if (v >= -1 && v < i) return (int16_t)v;
+      const int kid = tid - 128;
+      int32_t up = -1;
+      if (u.k1 > u.KT && kid < u.n) {  // the parents, ahead of their use
+        up = p.parent[(int64_t)u.b * p.N + kid];
+        if (up < -1 || up >= kid) {
           dev::set_error(p.err, TRIA_DEVERR_TREE);
-          return -1;
-        };
-        up0 = fetch(row);
-        up1 = fetch(row + 128);
+          up = -1;
+        }
       }
       float mr = -INFINITY, l = 0.0f;
       uint32_t hurt[2][4] = {};  // nodes on this row's path whose V has Inf or NaN
       for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
         const int buf = MT == 2 ? m : x & 1;
-        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        uint32_t seen[HK / 32];
+#pragma unroll
+        for (int e = 0; e < HK / 32; ++e) seen[e] = ~0u;
         const bool draft = kt >= u.KT;
         const int valid = draft ? u.n - (kt - u.KT) * kTile : u.T - kt * kTile;  // columns (may pass 128)
         const bool masked = draft || valid < kTile;
@@ -516,13 +544,11 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
           tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
           uint8_t *vt = sm + S::OFF_RING + s * TB;
           if (draft) {
-            constexpr int ALL = 128 * MT;
+            constexpr int ALL = 128 * NH * MT;
+            static_assert(ALL >= TRIA_MAX_NODES, "a thread per parent");
             dev::named_barrier(1, ALL);  // the last tile's marks have been read
-            if (m == 0) {
-              if (row < 4) c.poison[row] = 0;
-              c.parent[row] = up0;
-              c.parent[row + 128] = up1;
-            }
+            if (kid < 4) c.poison[kid] = 0;
+            if (kid < TRIA_MAX_NODES) c.parent[kid] = (int16_t)up;
             dev::named_barrier(1, ALL);
             for (int i = tid - 128; i < kTile * D / 8; i += ALL) {
               uint4 *at = reinterpret_cast<uint4 *>(vt) + i;
@@ -554,60 +580,71 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
             dev::named_barrier(1, ALL);
             // the columns on this row's path
             const int j0 = (kt - u.KT) * kTile;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) seen[e] = 0u;
+            uint32_t on[4] = {0u, 0u, 0u, 0u};
             if (live)
               for (int j = node; j >= j0; j = c.parent[j]) {
                 const int q = j - j0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if ((q >> 5) == e) seen[e] |= 1u << (q & 31);
+                  if ((q >> 5) == e) on[e] |= 1u << (q & 31);
               }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j0) hurt[1][e] = seen[e] & c.poison[e];
-              else hurt[0][e] = seen[e] & c.poison[e];
+            for (int e = 0; e < 4; ++e) {
+              if (j0) hurt[1][e] = on[e] & c.poison[e];
+              else hurt[0][e] = on[e] & c.poison[e];
+            }
+#pragma unroll
+            for (int e = 0; e < HK / 32; ++e) seen[e] = NH == 2 && half ? on[2 + e] : on[e];
           } else {
-            for (int i = tid - 128 - 128 * m; i < (kTile - valid) * (D / 8); i += 128) {
+            for (int i = part_id; i < (kTile - valid) * (D / 8); i += 128 * NH) {
               const int r = valid + i / (D / 8), q = i % (D / 8);
               *(reinterpret_cast<uint4 *>(vt + (q >> 3) * SLAB + r * 128) + (q & 7)) =
                   make_uint4(0u, 0u, 0u, 0u);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              seen[e] = valid >= 32 * (e + 1) ? ~0u : valid <= 32 * e ? 0u : (1u << (valid - 32 * e)) - 1u;
+            for (int e = 0; e < HK / 32; ++e) {
+              const int v = valid - half * HK - 32 * e;
+              seen[e] = v >= 32 ? ~0u : v <= 0 ? 0u : (1u << v) - 1u;
+            }
           }
         }
         tree_wait(c, &c.s_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
         __syncwarp();
         tc::fence_after();
         if (any) {
-          float s[kTile];
+          float s[HK];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            tc::ld32(tm_s[buf] + lane_off + 32 * e, reinterpret_cast<uint32_t *>(s) + 32 * e);
+          for (int e = 0; e < HK / 32; ++e)
+            tc::ld32(tm_s[buf] + lane_off + half * HK + 32 * e, reinterpret_cast<uint32_t *>(s) + 32 * e);
           tc::wait_ld();
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < HK / 32; ++e)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(seen[e] >> i & 1u)) s[32 * e + i] = -INFINITY;
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 4; i < kTile; i += 4)
+          for (int i = 4; i < HK; i += 4)
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[i + e]);
-          const float mn = fmaxf(mr, sl * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // the row's other half; both have read their S by then, so P may overwrite it
+          if (NH == 2) {
+            c.swap[x & 1][m][half][row] = mx[0];
+            dev::named_barrier(pair, 64);
+            mx[0] = fmaxf(mx[0], c.swap[x & 1][m][half ^ 1][row]);
+          }
+          const float mn = fmaxf(mr, sl * mx[0]);
           if (__any_sync(0xffffffffu, mn > mr + 8.0f)) {
             const float a = mr == -INFINITY ? 0.0f : exp2_approx(mr - mn);
             if (kt > u.k0) {
               outputs_before(x);
               tc::fence_after();
 #pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
+              for (int d = half * HD; d < (half + 1) * HD; d += 32) {
                 uint32_t o[32];
                 tc::ld32(tm_o[m] + lane_off + d, o);
                 tc::wait_ld();
@@ -622,7 +659,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
           const float base = mr == -INFINITY ? 0.0f : mr;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < HK / 64; ++e) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -632,7 +669,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
               sum[(2 * i + 1) & 3] += a1;
               w[i] = pack_bf16x2(a0, a1);
             }
-            tc::st32(tm_s[buf] + lane_off + 32 * e, w);
+            tc::st32(tm_s[buf] + lane_off + (HK / 2) * half + 32 * e, w);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tc::wait_st();
@@ -642,19 +679,25 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         dev::mbar_arrive(&c.p_full[buf]);
       }
       // ------------------------------------------------------------ the unit, or its part
+      if (any && NH == 2) {  // the row's sum
+        c.swap[x & 1][m][half][row] = l;
+        dev::named_barrier(pair, 64);
+        const float other = c.swap[x & 1][m][half ^ 1][row];
+        l = half ? other + l : l + other;
+      }
       outputs_before(x);
       tc::fence_after();
       const bool whole = u.k0 == 0 && u.k1 == u.K;
-      float *part = p.scratch + ((size_t)cta * kPartSlots + (u.k0 > 0 ? 0 : 1)) * (size_t)(MT * kTile) * (D + 2);
       const int r = m * kTile + row;
       if (any) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint4 *to = reinterpret_cast<uint4 *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D);
+        float *part = p.scratch + ((size_t)cta * kPartSlots + (u.k0 > 0 ? 0 : 1)) * (size_t)(MT * kTile) * (D + 2) + r;
         bool any_hurt = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e) any_hurt |= (hurt[0][e] | hurt[1][e]) != 0;
 #pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
+        for (int d = half * HD; d < (half + 1) * HD; d += 32) {
           float o[32];
           __syncwarp();
           tc::ld32(tm_o[m] + lane_off + d, reinterpret_cast<uint32_t *>(o));
@@ -680,21 +723,22 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
                                            pack_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
           } else if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) part[(size_t)(d + i) * (MT * kTile) + r] = o[i];
+            for (int i = 0; i < 32; ++i) part[(d + i) * (MT * kTile)] = o[i];
           }
         }
-        if (!whole && live) {
-          part[(size_t)D * (MT * kTile) + r] = mr;
-          part[(size_t)(D + 1) * (MT * kTile) + r] = l;
+        if (!whole && live && half == 0) {
+          part[D * (MT * kTile)] = mr;
+          part[(D + 1) * (MT * kTile)] = l;
         }
       }
       tc::fence_before();
       dev::mbar_arrive(&c.o_free[m]);
-      // the unit goes on in the next CTAs: what the merge needs to know
-      if (m == 0 && row == 0 && u.k0 == 0 && u.k1 < u.K) {
+      // whether the unit goes on in the next CTAs: what the merge needs to know
+      if (m == 0 && part_id == 0 && u.k0 == 0 && (u.k1 < u.K || p.by_unit)) {
         const int64_t end = (int64_t)w0 + x - (u.k1 - u.k0) + u.K;  // past the unit's last tile
-        TreeDesc d = {u.b, u.g, u.mg, u.n, (int32_t)((end * ctas + total - 1) / total) - 1};
-        p.desc[cta] = d;
+        TreeDesc d = {u.k1 < u.K ? u.b : -1, u.g, u.mg, u.n, cta, (int32_t)((end * ctas + total - 1) / total) - 1};
+        const int M = (p.N * p.G + MT * kTile - 1) / (MT * kTile);
+        p.desc[p.by_unit ? (u.b * p.Hkv + u.g) * M + u.mg : cta] = d;
       }
     }
   }
@@ -705,67 +749,76 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   if (warp == 1) tc::tmem_free<512>(tmem);
 }
 
-// Merges the parts of the units that more than one CTA worked on: block (c, y, e) takes 32
-// rows and kMergeDims output dims of the unit that CTA c's share ends in.  Lane = row; warp w
-// adds up the parts w, w + 8, ... (a serial pass over the parts is bound by the latency of
-// its loads), and the warps' sums meet in shared memory, in the order of the warps.
-constexpr int kMergeDims = 64, kMergeWarps = 8;
+// Merges the parts of the units that more than one CTA worked on: block (e, y, z) takes 32
+// rows and p.merge_dims output dims of the unit of entry e, 16 dims at a time.  Lane = row;
+// warp w adds up the parts w, w + 8, ... with a running maximum (a serial pass over the parts
+// is bound by the latency of its loads), and the warps' sums meet in shared memory, in the
+// order of the warps.
+constexpr int kMergeStep = 16, kMergeWarps = 8;
 
 template <int D, int MT>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     tree_merge_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int ROWS = MT * kTile, DC = 16;  // dims per pass
+  constexpr int ROWS = MT * kTile, DC = kMergeStep;
   constexpr size_t PART = (size_t)ROWS * (D + 2);
   __shared__ float sm_o[kMergeWarps][DC][33], sm_l[kMergeWarps][32], sm_m[kMergeWarps][32];
   dev::pdl_wait();
-  const int c0 = blockIdx.x;
-  const TreeDesc u = p.desc[c0];
+  const TreeDesc u = p.desc[blockIdx.x];
   if (u.b < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = kTile / p.G;
-  // row r of the unit: node, head; rows past the nodes read a part's other rows and write nothing
+  const int per = kTile / p.G, node0 = u.mg * MT * per;
   const int r = blockIdx.y * 32 + lane;
-  const int node = u.mg * MT * per + r / p.G, head = u.g * p.G + r % p.G;
-  if (u.mg * MT * per + (int)blockIdx.y * 32 / p.G >= u.n) return;
+  const int node = node0 + r / p.G, head = u.g * p.G + r % p.G;
+  if (node0 + (int)blockIdx.y * 32 / p.G >= u.n) return;
   const bool live = node < u.n;
-  auto part = [&](int ct) { return p.scratch + ((size_t)ct * kPartSlots + (ct == c0 ? 1 : 0)) * PART + r; };
-  float M = -INFINITY;
-  if (live)
-    for (int ct = c0 + warp; ct <= u.last; ct += kMergeWarps) M = fmaxf(M, part(ct)[(size_t)D * ROWS]);
-  sm_m[warp][lane] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, sm_m[w][lane]);
-  if (M == -INFINITY) M = 0.0f;
+  auto part = [&](int ct) { return p.scratch + ((size_t)ct * kPartSlots + (ct == u.first ? 1 : 0)) * PART + r; };
 #pragma unroll 1
-  for (int d0 = blockIdx.z * kMergeDims; d0 < (int)(blockIdx.z + 1) * kMergeDims; d0 += DC) {
-    float L = 0.0f, o[DC] = {};
+  for (int d0 = blockIdx.z * p.merge_dims; d0 < (int)(blockIdx.z + 1) * p.merge_dims; d0 += DC) {
+    float M = -INFINITY, L = 0.0f, o[DC] = {};
     if (live)
-      for (int ct = c0 + warp; ct <= u.last; ct += kMergeWarps) {
-        const float *x = part(ct);
-        float v[DC];
+      for (int ct = u.first + warp; ct <= u.last; ct += 2 * kMergeWarps) {
+        const bool two = ct + kMergeWarps <= u.last;
+        const float *src[2] = {part(ct), part(two ? ct + kMergeWarps : ct)};
+        float v[2][DC], mc[2], l[2];
 #pragma unroll
-        for (int i = 0; i < DC; ++i) v[i] = x[(size_t)(d0 + i) * ROWS];
-        const float mc = x[(size_t)D * ROWS], l = x[(size_t)(D + 1) * ROWS];
+        for (int k = 0; k < 2; ++k) {
+          mc[k] = src[k][(size_t)D * ROWS];
+          l[k] = src[k][(size_t)(D + 1) * ROWS];
+#pragma unroll
+          for (int i = 0; i < DC; ++i) v[k][i] = src[k][(size_t)(d0 + i) * ROWS];
+        }
+        if (!two) mc[1] = -INFINITY;
+        const float mn = fmaxf(M, fmaxf(mc[0], mc[1]));
+        const float ref = mn == -INFINITY ? 0.0f : mn;
+        const float a = exp2_approx(M - ref);  // (0 for the first parts)
         // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
-        const float w = mc == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc - M);
-        L = fmaf(w, l, L);
+        const float w0 = mc[0] == -INFINITY ? (l[0] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc[0] - ref);
+        const float w1 = mc[1] == -INFINITY ? (!two || l[1] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc[1] - ref);
+        M = mn;
+        L = fmaf(L, a, fmaf(w0, l[0], two ? w1 * l[1] : 0.0f));
 #pragma unroll
-        for (int i = 0; i < DC; ++i) o[i] = fmaf(w, v[i], o[i]);
+        for (int i = 0; i < DC; ++i) o[i] = fmaf(o[i], a, fmaf(w0, v[0][i], two ? w1 * v[1][i] : 0.0f));
       }
     __syncthreads();  // the last pass has been read
+    sm_m[warp][lane] = M;
     sm_l[warp][lane] = L;
 #pragma unroll
     for (int i = 0; i < DC; ++i) sm_o[warp][i][lane] = o[i];
     __syncthreads();
     // thread (row, dim pair)
+    float ref = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) ref = fmaxf(ref, sm_m[w][lane]);
+    if (ref == -INFINITY) ref = 0.0f;
     L = 0.0f;
     float a = 0.0f, b = 0.0f;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
-      L += sm_l[w][lane];
-      a += sm_o[w][2 * warp][lane];
-      b += sm_o[w][2 * warp + 1][lane];
+      const float mw = sm_m[w][lane], lw = sm_l[w][lane];
+      const float k = mw == -INFINITY ? (lw == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - ref);
+      L = fmaf(k, lw, L);
+      a = fmaf(k, sm_o[w][2 * warp][lane], a);
+      b = fmaf(k, sm_o[w][2 * warp + 1][lane], b);
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     if (live)
@@ -806,6 +859,9 @@ int m_tiles(int D, int G, int N) { return D < 256 && N * G > kTile ? 2 : 1; }
 
 size_t desc_bytes() { return ((size_t)device_sm_count() * sizeof(TreeDesc) + 255) / 256 * 256; }
 
+// Blocks of 32 rows that a unit has at most.
+int merge_rows(const TreeAttnParams &p, int mt) { return (std::min(p.N * p.G, mt * kTile) + 31) / 32; }
+
 template <int D, int MT>
 cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
   auto kern = tree_attention_kernel<D, MT>;
@@ -823,8 +879,7 @@ cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int rows = min(p.N * p.G, MT * kTile);
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(rows + 31) / 32, D / kMergeDims);
+  cfg.gridDim = dim3((unsigned)(p.by_unit ? p.by_unit : ctas), (unsigned)merge_rows(p, MT), D / p.merge_dims);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -862,6 +917,13 @@ cudaError_t launch_tree_attention(const TreeAttnParams &params, void *scratch, c
       !map_3d(&p.tq, p.q, p.D, p.Hq, (int64_t)p.B * p.N, p.G, kTile / p.G))
     return cudaErrorInvalidValue;
   const int sms = device_sm_count(), ctas = (int)(most < sms ? most : sms);
+  const int64_t units = (int64_t)p.B * p.Hkv * ((p.N * p.G + mt * kTile - 1) / (mt * kTile));
+  p.by_unit = units <= ctas ? (int)units : 0;
+  // the merge's blocks: as many as are resident at once (eight per SM), for few loads in a row
+  p.merge_dims = kMergeStep;
+  while (p.merge_dims < p.D &&
+         (int64_t)(p.by_unit ? p.by_unit : ctas) * merge_rows(p, mt) * (p.D / p.merge_dims) > 8 * sms)
+    p.merge_dims *= 2;
   if (p.D == 64) return mt == 2 ? launch<64, 2>(p, ctas, s) : launch<64, 1>(p, ctas, s);
   if (p.D == 128) return mt == 2 ? launch<128, 2>(p, ctas, s) : launch<128, 1>(p, ctas, s);
   return launch<256, 1>(p, ctas, s);

@@ -46,10 +46,6 @@
 #include "tcgen05.cuh"
 #include "tree.cuh"
 
-#ifndef TREE_NH2
-#define TREE_NH2 1
-#endif
-
 namespace tria {
 
 namespace {
@@ -66,7 +62,7 @@ struct TreeShape {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = QB * MT * TB;
   static constexpr int OFF_CTL = OFF_RING + NS * TB;
-  static constexpr int NH = MT == 2 ? TREE_NH2 : 2;      // threads per row
+  static constexpr int NH = MT == 2 ? 1 : 2;      // threads per row
   static constexpr int THREADS = 128 + 128 * NH * MT;
 };
 
@@ -77,7 +73,7 @@ struct TreeCtl {
   int32_t start_b, start_rem;          // where this CTA's share starts
   int32_t warp_sums[8];
   uint32_t poison[4];                  // drafted V rows of the tile with Inf or NaN
-  float swap[2][2][2][kTile];          // by tile parity, M tile and half: maxima, at the end sums
+  float swap[2][2][2][kTile];          // what a row's two threads exchange: in turn, by M tile and half
   uint32_t tn[TRIA_MAX_BATCH];         // live length (0 with per-unit lengths) << 9 | nodes (0: skipped)
   int16_t parent[TRIA_MAX_NODES];
 };
@@ -115,6 +111,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// Two float32 products and sums at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 // The tiles [k0, k1) of unit (b, g, mg), which has K tiles, KT of them cached.
 struct Piece {
@@ -215,8 +215,12 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   const int cta = blockIdx.x;
 
   // ---------------------------------------------------------------- setup
+  // (the segments' bounds by ordinary loads: a constant-bank read takes one address at a time)
+  const int64_t *starts = p.seg_start;
+  asm volatile("" : "+l"(starts));
   if (tid == 0) {
     dev::pdl_launch_dependents();
+    if (!p.by_unit) p.desc[cta].b = -1;
     const CUtensorMap *maps[] = {&p.tq, &p.tk, &p.tv, &p.tkd, &p.tvd};
     for (const CUtensorMap *t : maps)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(t)) : "memory");
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         bad = TRIA_DEVERR_TREE;
         n = 0;
       }
-      const int64_t cap_b = p.seg_start[tid + 1] - p.seg_start[tid];
+      const int64_t cap_b = starts[tid + 1] - starts[tid];
       const int M = (n * p.G + MT * kTile - 1) / (MT * kTile), DT = (n + kTile - 1) / kTile;
       if (p.unit_len) {
         for (int g = 0; g < p.Hkv; ++g) {
@@ -278,21 +282,6 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     if (lane >= o) incl += x;
   }
   if (warp < 8 && lane == 31) c.warp_sums[warp] = incl;
-  // the merge finds a unit that goes on in other CTAs by its number, or where there are more
-  // units than CTAs by the CTA that it starts in; the others' entries say that there is none
-  if (p.by_unit) {
-    if (cta == 0 && tid < p.by_unit) {
-      const int M = (p.N * p.G + MT * kTile - 1) / (MT * kTile);
-      const int mg = tid % M, b = tid / M / p.Hkv;
-      int32_t n = p.n_nodes[b];
-      if (n < 0 || n > p.N) n = 0;
-      const int32_t t = p.unit_len ? p.unit_len[((int64_t)p.layer * p.Hkv + tid / M % p.Hkv) * p.B + b] : p.seq_len[b];
-      if (mg * MT * kTile >= n * p.G || t < 0 || (int64_t)t > p.seg_start[b + 1] - p.seg_start[b])
-        p.desc[tid].b = -1;
-    }
-  } else if (tid == 0) {
-    p.desc[cta].b = -1;
-  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -313,6 +302,17 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   __syncthreads();
   const uint32_t tmem = c.tmem;
   const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + (MT == 2 ? D : 0)};
+
+  // The merge finds a unit that goes on in other CTAs by its number, or where there are more
+  // units than CTAs by the CTA that it starts in; the other entries say that there is none.
+  if (cta == 0 && (warp == 2 || warp == 3))
+    for (int i = tid - 64; i < p.by_unit; i += 64) {
+      const int M = (p.N * p.G + MT * kTile - 1) / (MT * kTile);
+      const int mg = i % M, g = i / M % p.Hkv, b = i / M / p.Hkv;
+      const int n = (int)(c.tn[b] & 511u);
+      const int32_t t = p.unit_len ? p.unit_len[((int64_t)p.layer * p.Hkv + g) * p.B + b] : 0;
+      if (mg * MT * kTile >= n * p.G || t < 0 || (int64_t)t > starts[b + 1] - starts[b]) p.desc[i].b = -1;
+    }
 
   if (X > 0) {
   if (warp == 0) {
@@ -499,7 +499,9 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     const uint32_t pair = 2 + m * 4 + q4;                      // barrier of a row's two warps (NH = 2)
     Walk<MT> walk(p, c, X);
     Piece u;
-    int x = 0, o_seen = 0;
+    constexpr int ALL = 128 * NH * MT;
+    static_assert(ALL >= TRIA_MAX_NODES, "a thread per parent");
+    int x = 0, o_seen = 0, swaps = 0;
     // The products with V up to that of tile x - 1 have completed.  Every tile awaits that
     // before it hands over its own P (by then they have, as a rule): a barrier's parity tells
     // only the last two phases apart, so none may be passed over or left behind.
@@ -525,76 +527,167 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       uint32_t hurt[2][4] = {};  // nodes on this row's path whose V has Inf or NaN
       for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
         const int buf = MT == 2 ? m : x & 1;
-        uint32_t seen[HK / 32];
-#pragma unroll
-        for (int e = 0; e < HK / 32; ++e) seen[e] = ~0u;
         const bool draft = kt >= u.KT;
         const int valid = draft ? u.n - (kt - u.KT) * kTile : u.T - kt * kTile;  // columns (may pass 128)
         const bool masked = draft || valid < kTile;
+        uint32_t on[4] = {~0u, ~0u, ~0u, ~0u};  // the tile's columns that this row sees
+        if (draft) {
+          dev::named_barrier(1, ALL);  // the last tile's parents and marks have been read
+          if (kid < 4) c.poison[kid] = 0;
+          if (kid < TRIA_MAX_NODES) c.parent[kid] = (int16_t)up;
+          dev::named_barrier(1, ALL);
+          const int j0 = (kt - u.KT) * kTile;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) on[e] = 0u;
+          if (live)
+            for (int j = node; j >= j0; j = c.parent[j]) {
+              const int q = j - j0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((q >> 5) == e) on[e] |= 1u << (q & 31);
+            }
+        } else if (masked) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            on[e] = valid >= 32 * (e + 1) ? ~0u : valid <= 32 * e ? 0u : (1u << (valid - 32 * e)) - 1u;
+        }
+        tree_wait(c, &c.s_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
+        __syncwarp();
+        tc::fence_after();
+        if (any) {
+          const uint32_t ts = tm_s[buf] + lane_off;
+          // columns [32 e, 32 e + 32) of this thread's keys
+          auto columns = [&](int e, float *s) {
+            tc::ld32(ts + half * HK + 32 * e, reinterpret_cast<uint32_t *>(s));
+            tc::wait_ld();
+            if (masked) {
+              const uint32_t bits = NH == 2 && half ? on[2 + e] : on[e];
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1u)) s[i] = -INFINITY;
+            }
+          };
+          // the larger of the two threads' values
+          auto both = [&](float v) {
+            if (NH == 1) return v;
+            c.swap[swaps & 1][m][half][row] = v;
+            dev::named_barrier(pair, 64);
+            v = fmaxf(v, c.swap[swaps & 1][m][half ^ 1][row]);
+            ++swaps;
+            return v;
+          };
+          if (kt == u.k0) {  // the first maximum
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < HK / 32; ++e) {
+              float s[32];
+              columns(e, s);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[i]);
+            }
+            mr = ceilf(sl * both(fmaxf(mx[0], mx[1])));
+          }
+          // P with the maximum so far, which as a rule stands (within 2^8), 64 keys at a time;
+          // if theirs is larger, once more with that.  Maxima are rounded up to whole powers
+          // of two, so that a change of scale is exact.
+#pragma unroll
+          for (int h = 0; h < HK / 64; ++h) {
+            float2 sum;
+            uint32_t w[32];
+            for (;;) {
+              const float base = mr == -INFINITY ? 0.0f : mr;
+              const float2 scale2 = make_float2(sl, sl), base2 = make_float2(-base, -base);
+              float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+              float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float s[32];
+                columns(2 * h + e, s);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 y = fma2(make_float2(s[2 * i], s[2 * i + 1]), scale2, base2);
+                  mx[0] = fmaxf(mx[0], y.x);
+                  mx[1] = fmaxf(mx[1], y.y);
+                  const float2 a = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                  sums[i & 1] = add2(sums[i & 1], a);
+                  w[16 * e + i] = pack_bf16x2(a.x, a.y);
+                }
+              }
+              sum = add2(sums[0], sums[1]);
+              const float mn = fmaxf(mr, ceilf(base + both(fmaxf(mx[0], mx[1]))));
+              if (!__any_sync(0xffffffffu, mn > mr + 8.0f)) break;
+              const float a = mr == -INFINITY ? 0.0f : exp2_approx(mr - mn);
+              if (kt > u.k0) {
+                outputs_before(x);
+                tc::fence_after();
+#pragma unroll 1
+                for (int d = half * HD; d < (half + 1) * HD; d += 32) {
+                  uint32_t o[32];
+                  tc::ld32(tm_o[m] + lane_off + d, o);
+                  tc::wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                  tc::st32(tm_o[m] + lane_off + d, o);
+                }
+              }
+              if (h > 0) {  // and the tile's first half of P
+                uint32_t o[32];
+                tc::wait_st();
+                tc::ld32(ts, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = pack_bf16x2(dev::bf16lo(o[i]) * a, dev::bf16hi(o[i]) * a);
+                tc::st32(ts, o);
+              }
+              l *= a;
+              mr = mn;
+            }
+            l += sum.x + sum.y;
+            // (both threads of the row have read the S that this overwrites)
+            tc::st32(ts + (HK / 2) * half + 32 * h, w);
+          }
+        }
         if (masked) {
           // this tile's V in shared memory: rows past `valid` become zero, and in a tile of
           // nodes so do Inf and NaN
           const int seq = v_seq<MT>(x, X), s = seq % NS;
-          // (a ring of two: the tile before in this place, the last V or this K, may still be
-          // on its way)
-          if (NS < 4) {
-            outputs_before(x);
-            tree_wait(c, &c.s_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
-          }
+          outputs_before(x);  // (a ring of two: the tile before in this place has arrived)
           tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
           uint8_t *vt = sm + S::OFF_RING + s * TB;
           if (draft) {
-            constexpr int ALL = 128 * NH * MT;
-            static_assert(ALL >= TRIA_MAX_NODES, "a thread per parent");
-            dev::named_barrier(1, ALL);  // the last tile's marks have been read
-            if (kid < 4) c.poison[kid] = 0;
-            if (kid < TRIA_MAX_NODES) c.parent[kid] = (int16_t)up;
-            dev::named_barrier(1, ALL);
-            for (int i = tid - 128; i < kTile * D / 8; i += ALL) {
+            for (int i = kid; i < kTile * D / 8; i += ALL) {
               uint4 *at = reinterpret_cast<uint4 *>(vt) + i;
               const int r = (i >> 3) & (kTile - 1);
               if (r >= valid) {
                 *at = make_uint4(0u, 0u, 0u, 0u);
                 continue;
               }
-              uint4 w = *at;
-              uint32_t *ws = &w.x;
+              uint4 v = *at;
+              uint32_t *vs = &v.x;
               bool bad = false;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                if ((ws[e] & 0x7f80u) == 0x7f80u) {
-                  ws[e] &= 0xffff0000u;
+                if ((vs[e] & 0x7f80u) == 0x7f80u) {
+                  vs[e] &= 0xffff0000u;
                   bad = true;
                 }
-                if ((ws[e] & 0x7f800000u) == 0x7f800000u) {
-                  ws[e] &= 0x0000ffffu;
+                if ((vs[e] & 0x7f800000u) == 0x7f800000u) {
+                  vs[e] &= 0x0000ffffu;
                   bad = true;
                 }
               }
               if (bad) {
-                *at = w;
+                *at = v;
                 atomicOr(&c.poison[r >> 5], 1u << (r & 31));
               }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             dev::named_barrier(1, ALL);
-            // the columns on this row's path
-            const int j0 = (kt - u.KT) * kTile;
-            uint32_t on[4] = {0u, 0u, 0u, 0u};
-            if (live)
-              for (int j = node; j >= j0; j = c.parent[j]) {
-                const int q = j - j0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if ((q >> 5) == e) on[e] |= 1u << (q & 31);
-              }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (j0) hurt[1][e] = on[e] & c.poison[e];
+              if (kt > u.KT) hurt[1][e] = on[e] & c.poison[e];
               else hurt[0][e] = on[e] & c.poison[e];
             }
-#pragma unroll
-            for (int e = 0; e < HK / 32; ++e) seen[e] = NH == 2 && half ? on[2 + e] : on[e];
           } else {
             for (int i = part_id; i < (kTile - valid) * (D / 8); i += 128 * NH) {
               const int r = valid + i / (D / 8), q = i % (D / 8);
@@ -602,87 +695,19 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
                   make_uint4(0u, 0u, 0u, 0u);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-#pragma unroll
-            for (int e = 0; e < HK / 32; ++e) {
-              const int v = valid - half * HK - 32 * e;
-              seen[e] = v >= 32 ? ~0u : v <= 0 ? 0u : (1u << v) - 1u;
-            }
           }
-        }
-        tree_wait(c, &c.s_full[buf], (MT == 2 ? x : x >> 1) & 1, p.err);
-        __syncwarp();
-        tc::fence_after();
-        if (any) {
-          float s[HK];
-#pragma unroll
-          for (int e = 0; e < HK / 32; ++e)
-            tc::ld32(tm_s[buf] + lane_off + half * HK + 32 * e, reinterpret_cast<uint32_t *>(s) + 32 * e);
-          tc::wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < HK / 32; ++e)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(seen[e] >> i & 1u)) s[32 * e + i] = -INFINITY;
-          }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int i = 4; i < HK; i += 4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[i + e]);
-          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // the row's other half; both have read their S by then, so P may overwrite it
-          if (NH == 2) {
-            c.swap[x & 1][m][half][row] = mx[0];
-            dev::named_barrier(pair, 64);
-            mx[0] = fmaxf(mx[0], c.swap[x & 1][m][half ^ 1][row]);
-          }
-          const float mn = fmaxf(mr, sl * mx[0]);
-          if (__any_sync(0xffffffffu, mn > mr + 8.0f)) {
-            const float a = mr == -INFINITY ? 0.0f : exp2_approx(mr - mn);
-            if (kt > u.k0) {
-              outputs_before(x);
-              tc::fence_after();
-#pragma unroll 1
-              for (int d = half * HD; d < (half + 1) * HD; d += 32) {
-                uint32_t o[32];
-                tc::ld32(tm_o[m] + lane_off + d, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-                tc::st32(tm_o[m] + lane_off + d, o);
-              }
-            }
-            l *= a;
-            mr = mn;
-          }
-          const float base = mr == -INFINITY ? 0.0f : mr;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int e = 0; e < HK / 64; ++e) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float a0 = exp2_approx(fmaf(s[64 * e + 2 * i], sl, -base));
-              const float a1 = exp2_approx(fmaf(s[64 * e + 2 * i + 1], sl, -base));
-              sum[(2 * i) & 3] += a0;
-              sum[(2 * i + 1) & 3] += a1;
-              w[i] = pack_bf16x2(a0, a1);
-            }
-            tc::st32(tm_s[buf] + lane_off + (HK / 2) * half + 32 * e, w);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tc::wait_st();
         }
         outputs_before(x);
+        tc::wait_st();
         tc::fence_before();
         dev::mbar_arrive(&c.p_full[buf]);
       }
       // ------------------------------------------------------------ the unit, or its part
       if (any && NH == 2) {  // the row's sum
-        c.swap[x & 1][m][half][row] = l;
+        c.swap[swaps & 1][m][half][row] = l;
         dev::named_barrier(pair, 64);
-        const float other = c.swap[x & 1][m][half ^ 1][row];
+        const float other = c.swap[swaps & 1][m][half ^ 1][row];
+        ++swaps;
         l = half ? other + l : l + other;
       }
       outputs_before(x);

@@ -46,6 +46,10 @@
 #include "tcgen05.cuh"
 #include "tree.cuh"
 
+#ifndef TREE_NH2
+#define TREE_NH2 1
+#endif
+
 namespace tria {
 
 namespace {
@@ -62,7 +66,7 @@ struct TreeShape {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = QB * MT * TB;
   static constexpr int OFF_CTL = OFF_RING + NS * TB;
-  static constexpr int NH = MT == 2 ? 1 : 2;      // threads per row
+  static constexpr int NH = MT == 2 ? TREE_NH2 : 2;      // threads per row
   static constexpr int THREADS = 128 + 128 * NH * MT;
 };
 
@@ -87,7 +91,14 @@ constexpr int tree_smem() {
 // Waits that ran out make every later wait return at once; all roles then run through
 // their loops without issuing copies or products.
 __device__ __forceinline__ bool tree_wait(TreeCtl &c, uint64_t *bar, uint32_t parity, int32_t *err) {
-  if (dev::mbar_try_wait(bar, parity)) return true;
+  uint32_t done;  // a plain test first: most barriers have completed by the time they are awaited
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(dev::smem_addr(bar)), "r"(parity)
+      : "memory");
+  if (done) return true;
   for (uint32_t i = 0; i < 2000000u; ++i) {
     if (*reinterpret_cast<volatile int32_t *>(&c.abort)) return false;
     if (dev::mbar_try_wait(bar, parity)) return true;
@@ -426,12 +437,9 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       return !gone;
     };
     const uint32_t base_lo = __shfl_sync(0xffffffffu, dev::smem_addr(sm), 0);
-    // S of tile x, M tile m
-    auto scores = [&](int x, int m, bool first, bool last) {
-      const int qb = pa % QB, seq = k_seq<MT>(x), s = seq % NS, buf = MT == 2 ? m : x & 1;
-      if (first) await(&c.q_full[qb], pa / QB);
-      if (m == 0) await(&c.full[s], seq / NS);
-      if (!settled()) return;
+    // S of the tile ahead, x, M tile m
+    auto scores = [&](int x, int m) {
+      const int qb = pa % QB, s = k_seq<MT>(x) % NS, buf = MT == 2 ? m : x & 1;
       const uint64_t qd = tc::desc(base_lo + S::OFF_Q + (qb * MT + m) * TB, 16);
       const uint64_t kd = tc::desc(base_lo + S::OFF_RING + s * TB, 16);
 #pragma unroll
@@ -442,22 +450,29 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       tc::commit(&c.s_full[buf], one);
       if (m == MT - 1) {
         tc::commit(&c.empty[s], one);
-        if (last) tc::commit(&c.q_empty[qb], one);
+        if (ka + 1 == ua.k1) tc::commit(&c.q_empty[qb], one);
       }
     };
+    // its operands have arrived
+    auto await_scores = [&](int x, int m) {
+      if (m > 0) return;
+      if (ka == ua.k0) await(&c.q_full[pa % QB], pa / QB);
+      await(&c.full[k_seq<MT>(x) % NS], k_seq<MT>(x) / NS);
+    };
     // O of tile x, M tile m
-    auto output = [&](int x, int m, bool first, int pi) {
-      const int seq = v_seq<MT>(x, X), s = seq % NS, buf = MT == 2 ? m : x & 1;
-      await(&c.p_full[buf], MT == 2 ? x : x >> 1);
-      if (m == 0) await(&c.full[s], seq / NS);
-      if (first && pi > 0) await(&c.o_free[m], pi - 1);
-      if (!settled()) return;
+    auto output = [&](int x, int m, bool first) {
+      const int s = v_seq<MT>(x, X) % NS, buf = MT == 2 ? m : x & 1;
       const uint64_t vd = tc::desc(base_lo + S::OFF_RING + s * TB, SLAB);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
         tc::mma_ts(tm_o[m], tm_s[buf] + 8 * k, vd + (2048 >> 4) * k, tc::instr(D, true), !first || k > 0, one);
       tc::commit(&c.o_full[m], one);
       if (m == MT - 1) tc::commit(&c.empty[s], one);
+    };
+    auto await_output = [&](int x, int m, bool first, int pi) {
+      if (m == 0) await(&c.full[v_seq<MT>(x, X) % NS], v_seq<MT>(x, X) / NS);
+      if (first && pi > 0) await(&c.o_free[m], pi - 1);
+      await(&c.p_full[MT == 2 ? m : x & 1], MT == 2 ? x : x >> 1);
     };
     auto step_ahead = [&]() {
       if (++ka == ua.k1) {
@@ -468,15 +483,27 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         }
       }
     };
-    for (int m = 0; m < MT; ++m) scores(0, m, true, ka + 1 == ua.k1);
+    await_scores(0, 0);
+    if (settled())
+      for (int m = 0; m < MT; ++m) scores(0, m);
     step_ahead();
     int x = 0, pi = 0;
     while (walk.next(u)) {
       for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
         for (int m = 0; m < MT; ++m) {
-          if (MT == 1 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
-          output(x, m, kt == u.k0, pi);
-          if (MT == 2 && more) scores(x + 1, m, ka == ua.k0, ka + 1 == ua.k1);
+          if (MT == 1 && more) {
+            await_scores(x + 1, m);
+            if (settled()) scores(x + 1, m);
+          }
+          // (two M tiles: the next S goes out right behind the product with V, so its operands
+          // are awaited before the P)
+          const bool first = kt == u.k0;
+          if (MT == 2 && more) await_scores(x + 1, m);
+          await_output(x, m, first, pi);
+          if (settled()) {
+            output(x, m, first);
+            if (MT == 2 && more) scores(x + 1, m);
+          }
         }
         if (more) step_ahead();
       }
@@ -501,12 +528,12 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     Piece u;
     constexpr int ALL = 128 * NH * MT;
     static_assert(ALL >= TRIA_MAX_NODES, "a thread per parent");
-    int x = 0, o_seen = 0, swaps = 0;
-    // The products with V up to that of tile x - 1 have completed.  Every tile awaits that
-    // before it hands over its own P (by then they have, as a rule): a barrier's parity tells
-    // only the last two phases apart, so none may be passed over or left behind.
+    int x = 0, swaps = 0;
+    // The products with V up to that of tile x - 1 have completed.  (A parity tells only the
+    // last two phases of a barrier apart.  While this row's P of tile x is outstanding, that of
+    // x - 1 or x - 2 is the last that can have completed, as S of x came after x - 2.)
     auto outputs_before = [&](int x) {
-      for (; o_seen < x; ++o_seen) tree_wait(c, &c.o_full[m], o_seen & 1, p.err);
+      if (x > 0) tree_wait(c, &c.o_full[m], (x - 1) & 1, p.err);
       __syncwarp();
     };
     while (walk.next(u)) {
@@ -556,17 +583,25 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         tc::fence_after();
         if (any) {
           const uint32_t ts = tm_s[buf] + lane_off;
-          // columns [32 e, 32 e + 32) of this thread's keys
-          auto columns = [&](int e, float *s) {
+          // columns [32 e, 32 e + 32) of this thread's keys: asked for, and arrived
+          auto ask = [&](int e, float *s) {
             tc::ld32(ts + half * HK + 32 * e, reinterpret_cast<uint32_t *>(s));
-            tc::wait_ld();
-            if (masked) {
-              const uint32_t bits = NH == 2 && half ? on[2 + e] : on[e];
+          };
+          if (masked) {  // -inf into the columns that this row does not see
+#pragma unroll 1
+            for (int e = 0; e < HK / 32; ++e) {
+              const int w4 = e + (NH == 2 ? 2 * half : 0);
+              const uint32_t bits = w4 == 0 ? on[0] : w4 == 1 ? on[1] : w4 == 2 ? on[2] : on[3];
+              float s[32];
+              ask(e, s);
+              tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1u)) s[i] = -INFINITY;
+              tc::st32(ts + half * HK + 32 * e, reinterpret_cast<uint32_t *>(s));
             }
-          };
+            tc::wait_st();
+          }
           // the larger of the two threads' values
           auto both = [&](float v) {
             if (NH == 1) return v;
@@ -578,10 +613,11 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
           };
           if (kt == u.k0) {  // the first maximum
             float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < HK / 32; ++e) {
               float s[32];
-              columns(e, s);
+              ask(e, s);
+              tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[i]);
             }
@@ -590,7 +626,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
           // P with the maximum so far, which as a rule stands (within 2^8), 64 keys at a time;
           // if theirs is larger, once more with that.  Maxima are rounded up to whole powers
           // of two, so that a change of scale is exact.
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < HK / 64; ++h) {
             float2 sum;
             uint32_t w[32];
@@ -599,13 +635,16 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
               const float2 scale2 = make_float2(sl, sl), base2 = make_float2(-base, -base);
               float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
               float mx[2] = {-INFINITY, -INFINITY};
+              float s[2][32];
+              ask(2 * h, s[0]);
+              tc::wait_ld();
+              ask(2 * h + 1, s[1]);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float s[32];
-                columns(2 * h + e, s);
+                if (e == 1) tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  const float2 y = fma2(make_float2(s[2 * i], s[2 * i + 1]), scale2, base2);
+                  const float2 y = fma2(make_float2(s[e][2 * i], s[e][2 * i + 1]), scale2, base2);
                   mx[0] = fmaxf(mx[0], y.x);
                   mx[1] = fmaxf(mx[1], y.y);
                   const float2 a = make_float2(exp2_approx(y.x), exp2_approx(y.y));
@@ -651,7 +690,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
           // this tile's V in shared memory: rows past `valid` become zero, and in a tile of
           // nodes so do Inf and NaN
           const int seq = v_seq<MT>(x, X), s = seq % NS;
-          outputs_before(x);  // (a ring of two: the tile before in this place has arrived)
+          if (NS < 4) outputs_before(x);  // (a ring of two: the tile before in this place has arrived)
           tree_wait(c, &c.full[s], (seq / NS) & 1, p.err);
           uint8_t *vt = sm + S::OFF_RING + s * TB;
           if (draft) {
@@ -697,7 +736,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
         }
-        outputs_before(x);
+        if (kt + 1 == u.k1) outputs_before(x);  // for the wait below, while it is certain which phase is next
         tc::wait_st();
         tc::fence_before();
         dev::mbar_arrive(&c.p_full[buf]);

@@ -73,7 +73,7 @@ struct alignas(64) TreeAttnParams {
   int32_t *err;
   PageParams pages;
   int64_t cap;
-  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows, by_unit, merge_dims;
+  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows, by_unit, merge_dims, merge_groups;
   float scale;
   int64_t seg_start[TRIA_MAX_BATCH + 1];
 };

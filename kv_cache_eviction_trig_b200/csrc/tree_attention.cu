@@ -814,22 +814,23 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
 }
 
 // Merges the parts of the units that more than one CTA worked on: block (e, y, z) takes 32
-// rows and p.merge_dims output dims of the unit of entry e, 16 dims at a time.  Lane = row;
-// warp w adds up the parts w, w + 8, ... with a running maximum (a serial pass over the parts
-// is bound by the latency of its loads), and the warps' sums meet in shared memory, in the
-// order of the warps.
+// rows and p.merge_dims output dims of the unit of entry e.  Lane = row.  The block's eight
+// warps are PG groups of parts (group w takes the parts w, w + PG, ... with a running maximum)
+// by 8 / PG groups of 16 dims; the groups' sums meet in shared memory, in the order of the
+// groups.  Bound by the latency of its loads: many parts want many groups (PG = 8), two or
+// three (more units than half the CTAs) few passes over the dims (PG = 2).
 constexpr int kMergeStep = 16, kMergeWarps = 8;
 
-template <int D, int MT>
+template <int D, int MT, int PG>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     tree_merge_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int ROWS = MT * kTile, DC = kMergeStep;
+  constexpr int ROWS = MT * kTile, DC = kMergeStep, DG = kMergeWarps / PG;
   constexpr size_t PART = (size_t)ROWS * (D + 2);
-  __shared__ float sm_o[kMergeWarps][DC][33], sm_l[kMergeWarps][32], sm_m[kMergeWarps][32];
+  __shared__ float sm_o[PG][DG * DC][33], sm_l[PG][32], sm_m[PG][32];
   dev::pdl_wait();
   const TreeDesc u = p.desc[blockIdx.x];
   if (u.b < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pg = warp / DG, dg = warp % DG;
   const int per = kTile / p.G, node0 = u.mg * MT * per;
   const int r = blockIdx.y * 32 + lane;
   const int node = node0 + r / p.G, head = u.g * p.G + r % p.G;
@@ -837,19 +838,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const bool live = node < u.n;
   auto part = [&](int ct) { return p.scratch + ((size_t)ct * kPartSlots + (ct == u.first ? 1 : 0)) * PART + r; };
 #pragma unroll 1
-  for (int d0 = blockIdx.z * p.merge_dims; d0 < (int)(blockIdx.z + 1) * p.merge_dims; d0 += DC) {
+  for (int d0 = blockIdx.z * p.merge_dims; d0 < (int)(blockIdx.z + 1) * p.merge_dims; d0 += DG * DC) {
+    const int d1 = d0 + dg * DC;
     float M = -INFINITY, L = 0.0f, o[DC] = {};
-    if (live)
-      for (int ct = u.first + warp; ct <= u.last; ct += 2 * kMergeWarps) {
-        const bool two = ct + kMergeWarps <= u.last;
-        const float *src[2] = {part(ct), part(two ? ct + kMergeWarps : ct)};
+    if (live && d1 < D)
+      for (int ct = u.first + pg; ct <= u.last; ct += 2 * PG) {
+        const bool two = ct + PG <= u.last;
+        const float *src[2] = {part(ct), part(two ? ct + PG : ct)};
         float v[2][DC], mc[2], l[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           mc[k] = src[k][(size_t)D * ROWS];
           l[k] = src[k][(size_t)(D + 1) * ROWS];
 #pragma unroll
-          for (int i = 0; i < DC; ++i) v[k][i] = src[k][(size_t)(d0 + i) * ROWS];
+          for (int i = 0; i < DC; ++i) v[k][i] = src[k][(size_t)(d1 + i) * ROWS];
         }
         if (!two) mc[1] = -INFINITY;
         const float mn = fmaxf(M, fmaxf(mc[0], mc[1]));
@@ -864,30 +866,42 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         for (int i = 0; i < DC; ++i) o[i] = fmaf(o[i], a, fmaf(w0, v[0][i], two ? w1 * v[1][i] : 0.0f));
       }
     __syncthreads();  // the last pass has been read
-    sm_m[warp][lane] = M;
-    sm_l[warp][lane] = L;
+    if (dg == 0) {
+      sm_m[pg][lane] = M;
+      sm_l[pg][lane] = L;
+    }
 #pragma unroll
-    for (int i = 0; i < DC; ++i) sm_o[warp][i][lane] = o[i];
+    for (int i = 0; i < DC; ++i) sm_o[pg][dg * DC + i][lane] = o[i];
     __syncthreads();
-    // thread (row, dim pair)
-    float ref = -INFINITY;
+    // warp w sums up the dims [2 DG w, 2 DG (w + 1)) of every row
+    float k[PG], ref = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) ref = fmaxf(ref, sm_m[w][lane]);
+    for (int w = 0; w < PG; ++w) ref = fmaxf(ref, sm_m[w][lane]);
     if (ref == -INFINITY) ref = 0.0f;
     L = 0.0f;
-    float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
+    for (int w = 0; w < PG; ++w) {
       const float mw = sm_m[w][lane], lw = sm_l[w][lane];
-      const float k = mw == -INFINITY ? (lw == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - ref);
-      L = fmaf(k, lw, L);
-      a = fmaf(k, sm_o[w][2 * warp][lane], a);
-      b = fmaf(k, sm_o[w][2 * warp + 1][lane], b);
+      k[w] = mw == -INFINITY ? (lw == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - ref);
+      L = fmaf(k[w], lw, L);
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    if (live)
-      reinterpret_cast<uint32_t *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D + d0)[warp] =
-          pack_bf16x2(a * inv, b * inv);
+    uint32_t y[DG];
+#pragma unroll
+    for (int j = 0; j < DG; ++j) {
+      float a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int w = 0; w < PG; ++w) {
+        a = fmaf(k[w], sm_o[w][2 * (DG * warp + j)][lane], a);
+        b = fmaf(k[w], sm_o[w][2 * (DG * warp + j) + 1][lane], b);
+      }
+      y[j] = pack_bf16x2(a * inv, b * inv);
+    }
+    if (live && d0 + 2 * DG * warp < D) {
+      uint32_t *to = reinterpret_cast<uint32_t *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D + d0) + DG * warp;
+      if constexpr (DG == 4) *reinterpret_cast<uint4 *>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+      else to[0] = y[0];
+    }
   }
 }
 
@@ -943,7 +957,7 @@ cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.by_unit ? p.by_unit : ctas), (unsigned)merge_rows(p, MT), D / p.merge_dims);
+  cfg.gridDim = dim3((unsigned)(p.by_unit ? p.by_unit : ctas), (unsigned)merge_rows(p, MT), (D + p.merge_dims - 1) / p.merge_dims);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -951,7 +965,8 @@ cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, MT>, p);
+  return p.merge_groups == 8 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, MT, 8>, p)
+                             : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, MT, 2>, p);
 }
 
 }  // namespace
@@ -984,7 +999,8 @@ cudaError_t launch_tree_attention(const TreeAttnParams &params, void *scratch, c
   const int64_t units = (int64_t)p.B * p.Hkv * ((p.N * p.G + mt * kTile - 1) / (mt * kTile));
   p.by_unit = units <= ctas ? (int)units : 0;
   // the merge's blocks: as many as are resident at once (eight per SM), for few loads in a row
-  p.merge_dims = kMergeStep;
+  p.merge_groups = 2 * units >= ctas ? 2 : 8;
+  p.merge_dims = kMergeStep * kMergeWarps / p.merge_groups;
   while (p.merge_dims < p.D &&
          (int64_t)(p.by_unit ? p.by_unit : ctas) * merge_rows(p, mt) * (p.D / p.merge_dims) > 8 * sms)
     p.merge_dims *= 2;

@@ -715,8 +715,10 @@ tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
   tp.D = cfg->head_dim;
   tp.scale = scale > 0.0f ? scale : 1.0f / std::sqrt((float)cfg->head_dim);
   for (int b = 0; b <= cfg->batch; ++b) tp.seg_start[b] = cache->seq_start[b];
-  return cuda_status(launch_tree_attention(tp, static_cast<uint8_t *>(ws) + kWsPrefix,
-                                           static_cast<cudaStream_t>(stream)));
+  tp.scratch = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsPrefix);
+  // the counters live in the workspace's zero-at-rest prefix
+  tp.arrived = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsHist);
+  return cuda_status(launch_tree_attention(tp, static_cast<cudaStream_t>(stream)));
 }
 
 tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,

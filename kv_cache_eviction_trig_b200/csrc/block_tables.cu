@@ -1,13 +1,19 @@
 // Block tables and slot maps of a paged cache from the lengths on the GPU (the pruned cache
 // in a paged KV cache: dimensionstp.github.io review, section 6, Limitations).
 //
-// One block: thread b < B works out what sequence b needs, two prefix sums over the
-// sequences give every block that changes hands its place in the pool's ring, and groups
-// of warps move a sequence's blocks: those past the need to the ring's tail, then, after a
-// barrier, the missing ones from its head.  A second grid (chained by programmatic
-// dependent launch) maps the tokens to slots; few slots are mapped by the first one.
-// Latency bound: the table rows and lengths of a decode step are a few KB.
+// One cluster: in every CTA thread b < B works out what sequence b needs, and two prefix sums
+// over the sequences give every block that changes hands its place in the pool's ring.  Groups
+// of warps, over all CTAs, move a sequence's blocks: those past the need to the ring's tail,
+// then, after a cluster barrier, the missing ones from its head.  A second grid (chained by
+// programmatic dependent launch) maps the tokens to slots; few slots are mapped by the first.
+// Bound by latency: the lengths, the blocks that change hands, the barrier.  Eight CTAs where
+// the table is large (kTableWide entries), as one CTA's warps take long rows one after
+// another; a single one, whose barriers are cheaper, below that.
+#include <cooperative_groups.h>
+
 #include "tree.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace tria {
 
@@ -15,7 +21,9 @@ namespace {
 
 constexpr int kTableThreads = 1024;
 constexpr int kMapThreads = 256;
-constexpr int64_t kMapInline = 8192;  // slots that the first block maps itself
+constexpr int64_t kMapInline = 8192;  // slots that the first grid maps itself
+constexpr int kTableCluster = 8;
+constexpr int64_t kTableWide = 8192;
 
 struct Ask {
   int32_t len, n;
@@ -68,15 +76,22 @@ __device__ __forceinline__ void scan2(int32_t (&v)[2], int32_t (*sums)[2]) {
   }
 }
 
+template <int CL>
 __global__ void __launch_bounds__(kTableThreads)
     block_tables_kernel(const __grid_constant__ BlockTablesParams p, int map_inline) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank();
+  auto sync = [&]() {
+    if (CL > 1) cl.sync();
+    else __syncthreads();
+  };
   // per sequence: what it holds, what it gets to hold, its places among the blocks that
   // are released and taken
   __shared__ int32_t s_old[TRIA_MAX_BATCH], s_new[TRIA_MAX_BATCH], s_rel[TRIA_MAX_BATCH],
       s_take[TRIA_MAX_BATCH], s_len[TRIA_MAX_BATCH], s_n[TRIA_MAX_BATCH];
   __shared__ int32_t sums[kTableThreads / 32][2], totals[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kWarps = kTableThreads / 32;
+  constexpr int kWarps = CL * kTableThreads / 32;
   if (tid == 0) dev::pdl_launch_dependents();
   const int32_t head = p.ring_state[0], count = p.ring_state[1];
   int32_t old = 0, need = 0, v[2] = {0, 0}, bad = 0;
@@ -119,11 +134,12 @@ __global__ void __launch_bounds__(kTableThreads)
     s_n[tid] = a.ok && (int64_t)a.len + a.n <= ((int64_t)need << p.shift) ? a.n : -1;
   }
   if (tid == 0 && !ring_ok) bad |= TRIA_DEVERR_PAGES;
-  if (bad) dev::set_error(p.err, bad);
+  if (bad && rank == 0) dev::set_error(p.err, bad);
   __syncthreads();
   // a group of warps per sequence
-  const int per = max(1, kWarps / p.B), group = warp / per, groups = kWarps / per;
-  const int first = (warp - group * per) * 32 + lane, step = per * 32;
+  const int all = rank * (kTableThreads / 32) + warp;
+  const int per = max(1, kWarps / p.B), group = all / per, groups = kWarps / per;
+  const int first = (all - group * per) * 32 + lane, step = per * 32;
   for (int b = group; b < p.B; b += groups) {
     const int32_t n0 = s_new[b], n1 = s_old[b];
     if (n1 <= n0) continue;
@@ -134,7 +150,7 @@ __global__ void __launch_bounds__(kTableThreads)
       row[j] = -1;
     }
   }
-  __syncthreads();  // what was released can be taken
+  sync();  // what was released can be taken, and every CTA has read the counts and the ring's state
   for (int b = group; b < p.B; b += groups) {
     const int32_t n0 = s_old[b], n1 = s_new[b];
     int32_t *row = p.table + (int64_t)b * p.max_blocks;
@@ -145,9 +161,8 @@ __global__ void __launch_bounds__(kTableThreads)
       row[j] = id;
     }
   }
-  if (tid < p.B) p.held[tid] = s_new[tid];
-  __syncthreads();  // the rows are complete
-  if (warp == 0) {
+  if (rank == 0 && tid < p.B) p.held[tid] = s_new[tid];
+  if (rank == 0 && warp == 0) {
     int32_t all = 0;
     for (int b = lane; b < p.B; b += 32) all += max(0, s_new[b] - s_old[b]);
     all = __reduce_add_sync(0xffffffffu, all);
@@ -157,6 +172,7 @@ __global__ void __launch_bounds__(kTableThreads)
     }
   }
   if (!map_inline) return;
+  sync();  // the rows are complete
   for (int b = group; b < p.B; b += groups) map_row(p, b, s_len[b], s_n[b], s_n[b] >= 0, first, step);
 }
 
@@ -175,19 +191,27 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const __grid_cons
 
 cudaError_t launch_block_tables(const BlockTablesParams &p, cudaStream_t s) {
   const bool small = (int64_t)p.B * p.max_new <= kMapInline;
-  block_tables_kernel<<<1, kTableThreads, 0, s>>>(p, small ? 1 : 0);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || small) return e;
-  const int64_t per = ((int64_t)p.max_new + kMapThreads - 1) / kMapThreads;
+  const bool wide = (int64_t)p.B * p.max_blocks > kTableWide;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(per < 1024 ? per : 1024), (unsigned)p.B, 1);
-  cfg.blockDim = dim3(kMapThreads, 1, 1);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(wide ? kTableCluster : 1, 1, 1);
+  cfg.blockDim = dim3(kTableThreads, 1, 1);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = wide ? kTableCluster : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, block_tables_kernel<kTableCluster>, p, small ? 1 : 0)
+                             : cudaLaunchKernelEx(&cfg, block_tables_kernel<1>, p, small ? 1 : 0);
+  if (e != cudaSuccess || small) return e;
+  const int64_t per = ((int64_t)p.max_new + kMapThreads - 1) / kMapThreads;
+  cfg.gridDim = dim3((unsigned)(per < 1024 ? per : 1024), (unsigned)p.B, 1);
+  cfg.blockDim = dim3(kMapThreads, 1, 1);
+  attr[0] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, slot_map_kernel, p);
 }
 

@@ -48,18 +48,12 @@ struct TreeCommitParams {
 };
 cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t s);
 
-// A unit of the attention (sequence, KV head, group of M tiles) whose key tiles lie in more
-// than one CTA's share, for the merge.
-struct alignas(32) TreeDesc {
-  int32_t b, g, mg, n, first, last;  // b < 0: none; n: its nodes; the CTAs that it starts and ends in
-};
-
 struct alignas(64) TreeAttnParams {
   CUtensorMap tk, tv;       // K and V as [L*Hkv][cap][D], boxes of 64 columns x 128 rows (or a block)
   CUtensorMap tkd, tvd;     // the nodes' as [L*Hkv*B][N][D], boxes of 64 x draft_rows
   CUtensorMap tq;           // the queries as [B*N][Hq][D], boxes of 64 x G heads x 128 / G nodes
-  TreeDesc *desc;           // one per unit (by_unit of them) or, if that is 0, per CTA
   float *scratch;           // two parts per CTA: unnormalised output [D][rows], maxima, sums
+  int32_t *arrived;         // per CTA, a line apart: reports on the unit that starts there; zero at rest
   const int32_t *parent;    // [B][N]
   const int32_t *n_nodes;   // [B]
   const uint16_t *q;        // bf16 [B][N][Hq][D]
@@ -73,13 +67,13 @@ struct alignas(64) TreeAttnParams {
   int32_t *err;
   PageParams pages;
   int64_t cap;
-  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows, by_unit, merge_dims, merge_groups;
+  int32_t layer, L, B, N, Hkv, Hq, G, D, draft_rows;
   float scale;
   int64_t seg_start[TRIA_MAX_BATCH + 1];
 };
 // The tensor maps and what depends on the launch are filled in here; scratch holds
 // tree_attention_scratch bytes.
-cudaError_t launch_tree_attention(const TreeAttnParams &p, void *scratch, cudaStream_t s);
+cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t s);
 size_t tree_attention_scratch(int D, int G, int N);
 
 }  // namespace tria

@@ -20,9 +20,12 @@
 // The next tile's S is computed while this one's softmax runs (MT = 1: two S buffers; MT = 2:
 // the M tiles alternate).  O stays in tensor memory and is rescaled only when a row's
 // maximum grew by more than 2^8 (P is at most 2^8 then; float32 sums lose nothing).
-// A unit that lies in one CTA is written from there; the parts of the others go to the
-// workspace with their maxima and sums, and a second kernel (chained by programmatic
-// dependent launch) merges them in the order of the keys, so results do not depend on timing.
+// A unit that lies in one CTA is written from there.  The parts of the others go to the
+// workspace with their maxima and sums; once a CTA is through with its share it waits for the
+// other CTAs of its first and of its last unit and merges its share of their rows and columns,
+// the parts in the order of the keys, so results do not depend on timing.  (The launch is
+// cooperative: all CTAs are resident, and each reports its parts before it waits.  A merge
+// kernel of its own took 7 us from the last part to the last row, this one 2 us.)
 //
 // Rounding: S, maxima, sums and O are float32.  P is rounded to bf16 for the product with
 // the bf16 V (its error is that of the bf16 output's own rounding); the sum is of the
@@ -56,6 +59,12 @@ namespace {
 
 constexpr int kTile = 128;   // keys per tile, rows per M tile
 constexpr int kPartSlots = 2;  // parts that a CTA can leave: of its first and of its last unit
+constexpr int kArriveStride = 32;  // words from one unit's counter to the next: a line each
+
+// A unit of which a CTA has a part.
+struct TreePart {
+  int32_t b, head0, node0, n, first, last;  // first, last: the CTAs with its first and last tile
+};
 
 template <int D, int MT>
 struct TreeShape {
@@ -74,7 +83,7 @@ struct TreeCtl {
   uint64_t full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], done;
   uint32_t tmem;
   int32_t abort;
-  int32_t start_b, start_rem;          // where this CTA's share starts
+  int4 start;                          // where this CTA's share starts: sequence, head, M group, tile
   int32_t warp_sums[8];
   uint32_t poison[4];                  // drafted V rows of the tile with Inf or NaN
   float swap[2][2][2][kTile];          // what a row's two threads exchange: in turn, by M tile and half
@@ -153,20 +162,7 @@ struct Walk {
     return T < 0 ? 0 : (T + kTile - 1) / kTile + (nodes(b_) + kTile - 1) / kTile;
   }
   __device__ __forceinline__ Walk(const TreeAttnParams &p_, const TreeCtl &c_, int left_)
-      : p(p_), c(c_), b(c_.start_b), g(0), mg(0), kt(0), left(left_) {
-    if (left <= 0) return;
-    int rem = c.start_rem;
-    const int M = groups(b);
-    for (g = 0; g < p.Hkv; ++g) {
-      const int K = tiles(b, length(b, g));
-      if (rem < K * M) {
-        mg = rem / K;
-        kt = rem - mg * K;
-        break;
-      }
-      rem -= K * M;
-    }
-  }
+      : p(p_), c(c_), b(c_.start.x), g(c_.start.y), mg(c_.start.z), kt(c_.start.w), left(left_) {}
   __device__ __forceinline__ bool next(Piece &x) {
     while (left > 0) {
       if (g == p.Hkv || nodes(b) == 0) {
@@ -214,6 +210,53 @@ __device__ __forceinline__ int64_t share_start(int64_t total, int c, int ctas) {
   return total * c / ctas;
 }
 
+// Merges a unit's parts, in the order of the keys: warp `rank` of `warps` takes every warps-th
+// item of 32 rows by DC output dims, lane = row, AT parts under way at a time (the loads'
+// latency bounds it: many parts want few dims at a time, few parts many).
+template <int D, int ROWS, int DC, int AT>
+__device__ __forceinline__ void merge_items(const TreeAttnParams &p, const TreePart &t, int rank, int warps) {
+  constexpr int PART = ROWS * (D + 2);
+  const int lane = threadIdx.x & 31, parts = t.last - t.first + 1;
+  const int rows = min((t.n - t.node0) * p.G, ROWS), groups = (rows + 31) / 32;
+  for (int it = rank; it < groups * (D / DC); it += warps) {
+    const int d0 = it / groups * DC, r = (it % groups) * 32 + lane;
+    if (r >= rows) continue;
+    const float *src = p.scratch + (size_t)t.first * kPartSlots * PART + r;
+    float M = -INFINITY, L = 0.0f, o[DC] = {};
+    for (int i0 = 0; i0 < parts; i0 += AT) {
+      float v[AT][DC + 2];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        if (i0 + i < parts) {
+          const float *y = src + ((size_t)(i0 + i) * kPartSlots + (i0 + i == 0 ? 1 : 0)) * PART;
+#pragma unroll
+          for (int e = 0; e < DC; ++e) v[i][e] = __ldcg(y + (d0 + e) * ROWS);
+          v[i][DC] = __ldcg(y + D * ROWS);
+          v[i][DC + 1] = __ldcg(y + (D + 1) * ROWS);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        if (i0 + i < parts) {
+          // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
+          const float mc = v[i][DC], l1 = v[i][DC + 1], top = fmaxf(M, mc), ref = top == -INFINITY ? 0.0f : top;
+          const float a = exp2_approx(M - ref);  // (0 for the first part)
+          const float w = mc == -INFINITY ? (l1 == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc - ref);
+          M = top;
+          L = fmaf(L, a, w * l1);
+#pragma unroll
+          for (int e = 0; e < DC; ++e) o[e] = fmaf(o[e], a, w * v[i][e]);
+        }
+      }
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint2 *to = reinterpret_cast<uint2 *>(p.out + (((int64_t)t.b * p.N + t.node0 + r / p.G) * p.Hq + t.head0 + r % p.G) * D + d0);
+#pragma unroll
+    for (int e = 0; e < DC; e += 4)
+      to[e / 4] = make_uint2(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv));
+  }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     tree_attention_kernel(const __grid_constant__ TreeAttnParams p) {
@@ -229,19 +272,15 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   // (the segments' bounds by ordinary loads: a constant-bank read takes one address at a time)
   const int64_t *starts = p.seg_start;
   asm volatile("" : "+l"(starts));
-  if (tid == 0) {
-    dev::pdl_launch_dependents();
-    if (!p.by_unit) p.desc[cta].b = -1;
+  if (tid == 96) {
     const CUtensorMap *maps[] = {&p.tq, &p.tk, &p.tv, &p.tkd, &p.tvd};
     for (const CUtensorMap *t : maps)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(t)) : "memory");
   }
   int tiles_b = 0;
   if (tid < TRIA_MAX_BATCH) {
-    int T = 0, n = 0;
     if (tid < p.B) {
-      n = p.n_nodes[tid];
-      int bad = 0;
+      int n = p.n_nodes[tid], T = p.unit_len ? 0 : p.seq_len[tid], bad = 0;
       if (n < 0 || n > p.N) {
         bad = TRIA_DEVERR_TREE;
         n = 0;
@@ -255,7 +294,6 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
           else tiles_b += M * ((t + kTile - 1) / kTile + DT);
         }
       } else {
-        T = p.seq_len[tid];
         if (T < 0 || (int64_t)T > cap_b) {
           bad |= TRIA_DEVERR_SEQ_LEN;
           n = T = 0;
@@ -268,7 +306,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     }
   }
   if (warp == 1) tc::tmem_alloc<512>(&c.tmem);
-  if (tid == 0) {
+  if (tid == 64) {
     for (int i = 0; i < NS; ++i) {
       dev::mbar_init(&c.full[i], 1);
       dev::mbar_init(&c.empty[i], 1);
@@ -307,23 +345,26 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   const int w1 = cta < ctas ? (int)share_start(total, cta + 1, ctas) : 0;
   const int X = w1 - w0;
   if (X > 0 && tid < TRIA_MAX_BATCH && w0 >= incl - tiles_b && w0 < incl) {
-    c.start_b = tid;
-    c.start_rem = w0 - (incl - tiles_b);
+    const int n = (int)(c.tn[tid] & 511u), M = (n * p.G + MT * kTile - 1) / (MT * kTile);
+    int rem = w0 - (incl - tiles_b), g = 0, K = (int)(c.tn[tid] >> 9);
+    K = (K + kTile - 1) / kTile + (n + kTile - 1) / kTile;
+    if (p.unit_len) {
+      for (;; ++g) {
+        const int32_t t = p.unit_len[((int64_t)p.layer * p.Hkv + g) * p.B + tid];
+        const bool fine = t >= 0 && (int64_t)t <= starts[tid + 1] - starts[tid];
+        K = fine ? (t + kTile - 1) / kTile + (n + kTile - 1) / kTile : 0;
+        if (rem < K * M) break;
+        rem -= K * M;
+      }
+    } else {
+      g = rem / (K * M);
+      rem -= g * K * M;
+    }
+    c.start = make_int4(tid, g, rem / K, rem % K);
   }
   __syncthreads();
   const uint32_t tmem = c.tmem;
   const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + (MT == 2 ? D : 0)};
-
-  // The merge finds a unit that goes on in other CTAs by its number, or where there are more
-  // units than CTAs by the CTA that it starts in; the other entries say that there is none.
-  if (cta == 0 && (warp == 2 || warp == 3))
-    for (int i = tid - 64; i < p.by_unit; i += 64) {
-      const int M = (p.N * p.G + MT * kTile - 1) / (MT * kTile);
-      const int mg = i % M, g = i / M % p.Hkv, b = i / M / p.Hkv;
-      const int n = (int)(c.tn[b] & 511u);
-      const int32_t t = p.unit_len ? p.unit_len[((int64_t)p.layer * p.Hkv + g) * p.B + b] : 0;
-      if (mg * MT * kTile >= n * p.G || t < 0 || (int64_t)t > starts[b + 1] - starts[b]) p.desc[i].b = -1;
-    }
 
   if (X > 0) {
   if (warp == 0) {
@@ -519,7 +560,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     // ---------------------------------------------------------------- softmax
     constexpr int NH = S::NH, HK = kTile / NH, HD = D / NH;    // keys and output dims per thread
     const int q4 = warp & 3, m = (warp - 4) / (4 * NH), half = NH == 2 ? ((warp - 4) >> 2) & 1 : 0;
-    const int row = q4 * 32 + lane, part_id = half * 128 + row;  // row of M tile m; its thread
+    const int kid = tid - 128, row = q4 * 32 + lane, part_id = half * 128 + row;  // row of M tile m; its thread
     const uint32_t lane_off = (uint32_t)q4 << 21;              // 32 lanes of tensor memory
     const float sl = p.scale * 1.4426950408889634f;            // logits in powers of two
     const int per = kTile / p.G;                               // nodes per M tile
@@ -529,6 +570,10 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     constexpr int ALL = 128 * NH * MT;
     static_assert(ALL >= TRIA_MAX_NODES, "a thread per parent");
     int x = 0, swaps = 0;
+    // the units of which this CTA has a part: what their merge needs
+    constexpr int ROWS = MT * kTile;
+    int pending = 0;
+    TreePart todo[2];
     // The products with V up to that of tile x - 1 have completed.  (A parity tells only the
     // last two phases of a barrier apart.  While this row's P of tile x is outstanding, that of
     // x - 1 or x - 2 is the last that can have completed, as S of x came after x - 2.)
@@ -541,7 +586,6 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       const int node = node0 + row / p.G, head = u.g * p.G + row % p.G;
       const bool live = node < u.n;
       const bool any = node0 + (row & ~31) / p.G < u.n;  // the warp has a live row
-      const int kid = tid - 128;
       int32_t up = -1;
       if (u.k1 > u.KT && kid < u.n) {  // the parents, ahead of their use
         up = p.parent[(int64_t)u.b * p.N + kid];
@@ -797,13 +841,40 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       }
       tc::fence_before();
       dev::mbar_arrive(&c.o_free[m]);
-      // whether the unit goes on in the next CTAs: what the merge needs to know
-      if (m == 0 && part_id == 0 && u.k0 == 0 && (u.k1 < u.K || p.by_unit)) {
-        const int64_t end = (int64_t)w0 + x - (u.k1 - u.k0) + u.K;  // past the unit's last tile
-        TreeDesc d = {u.k1 < u.K ? u.b : -1, u.g, u.mg, u.n, cta, (int32_t)((end * ctas + total - 1) / total) - 1};
-        const int M = (p.N * p.G + MT * kTile - 1) / (MT * kTile);
-        p.desc[p.by_unit ? (u.b * p.Hkv + u.g) * M + u.mg : cta] = d;
+      if (!whole) {  // reported once all threads have stored it
+        const int64_t from = (int64_t)w0 + x - (u.k1 - u.k0) - u.k0, to = from + u.K;  // the unit's tiles
+        TreePart &t = todo[pending++];
+        t.b = u.b;
+        t.head0 = u.g * p.G;
+        t.node0 = u.mg * MT * per;
+        t.n = u.n;
+        t.first = (int32_t)(((from + 1) * ctas + total - 1) / total) - 1;
+        t.last = (int32_t)((to * ctas + total - 1) / total) - 1;
+        __threadfence();
+        dev::named_barrier(1, ALL);
+        if (kid == 0) atomicAdd(p.arrived + t.first * kArriveStride, 1);
       }
+    }
+    // ---------------------------------------------------------------- merge
+    for (int k = 0; k < pending; ++k) {
+      const TreePart t = todo[k];
+      const int parts = t.last - t.first + 1;
+      int32_t *arrived = p.arrived + t.first * kArriveStride;
+      if (kid == 0) {
+        int32_t seen = 0;
+        for (uint32_t i = 0; i < 20000000u && seen < parts; ++i) {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(arrived) : "memory");
+          if (*reinterpret_cast<volatile int32_t *>(&c.abort)) break;
+        }
+        if (seen < parts) dev::set_error(p.err, TRIA_DEVERR_TIMEOUT);
+      }
+      dev::named_barrier(1, ALL);
+      // its items (32 rows by some output dims) over the warps of the unit's CTAs
+      const int rank = (cta - t.first) * (ALL / 32) + (kid >> 5);
+      if (parts > 4) merge_items<D, ROWS, MT == 2 ? 8 : 4, MT == 2 ? 8 : 10>(p, t, rank, parts * (ALL / 32));
+      else merge_items<D, ROWS, 16, 4>(p, t, rank, parts * (ALL / 32));
+      // the last of the unit's CTAs to be done leaves the counter at zero
+      if (kid == 0 && atomicAdd(arrived, 1) == 2 * parts - 1) atomicExch(arrived, 0);
     }
   }
   }
@@ -811,98 +882,6 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 1) tc::tmem_free<512>(tmem);
-}
-
-// Merges the parts of the units that more than one CTA worked on: block (e, y, z) takes 32
-// rows and p.merge_dims output dims of the unit of entry e.  Lane = row.  The block's eight
-// warps are PG groups of parts (group w takes the parts w, w + PG, ... with a running maximum)
-// by 8 / PG groups of 16 dims; the groups' sums meet in shared memory, in the order of the
-// groups.  Bound by the latency of its loads: many parts want many groups (PG = 8), two or
-// three (more units than half the CTAs) few passes over the dims (PG = 2).
-constexpr int kMergeStep = 16, kMergeWarps = 8;
-
-template <int D, int MT, int PG>
-__global__ void __launch_bounds__(kMergeWarps * 32)
-    tree_merge_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int ROWS = MT * kTile, DC = kMergeStep, DG = kMergeWarps / PG;
-  constexpr size_t PART = (size_t)ROWS * (D + 2);
-  __shared__ float sm_o[PG][DG * DC][33], sm_l[PG][32], sm_m[PG][32];
-  dev::pdl_wait();
-  const TreeDesc u = p.desc[blockIdx.x];
-  if (u.b < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pg = warp / DG, dg = warp % DG;
-  const int per = kTile / p.G, node0 = u.mg * MT * per;
-  const int r = blockIdx.y * 32 + lane;
-  const int node = node0 + r / p.G, head = u.g * p.G + r % p.G;
-  if (node0 + (int)blockIdx.y * 32 / p.G >= u.n) return;
-  const bool live = node < u.n;
-  auto part = [&](int ct) { return p.scratch + ((size_t)ct * kPartSlots + (ct == u.first ? 1 : 0)) * PART + r; };
-#pragma unroll 1
-  for (int d0 = blockIdx.z * p.merge_dims; d0 < (int)(blockIdx.z + 1) * p.merge_dims; d0 += DG * DC) {
-    const int d1 = d0 + dg * DC;
-    float M = -INFINITY, L = 0.0f, o[DC] = {};
-    if (live && d1 < D)
-      for (int ct = u.first + pg; ct <= u.last; ct += 2 * PG) {
-        const bool two = ct + PG <= u.last;
-        const float *src[2] = {part(ct), part(two ? ct + PG : ct)};
-        float v[2][DC], mc[2], l[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mc[k] = src[k][(size_t)D * ROWS];
-          l[k] = src[k][(size_t)(D + 1) * ROWS];
-#pragma unroll
-          for (int i = 0; i < DC; ++i) v[k][i] = src[k][(size_t)(d1 + i) * ROWS];
-        }
-        if (!two) mc[1] = -INFINITY;
-        const float mn = fmaxf(M, fmaxf(mc[0], mc[1]));
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float a = exp2_approx(M - ref);  // (0 for the first parts)
-        // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
-        const float w0 = mc[0] == -INFINITY ? (l[0] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc[0] - ref);
-        const float w1 = mc[1] == -INFINITY ? (!two || l[1] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc[1] - ref);
-        M = mn;
-        L = fmaf(L, a, fmaf(w0, l[0], two ? w1 * l[1] : 0.0f));
-#pragma unroll
-        for (int i = 0; i < DC; ++i) o[i] = fmaf(o[i], a, fmaf(w0, v[0][i], two ? w1 * v[1][i] : 0.0f));
-      }
-    __syncthreads();  // the last pass has been read
-    if (dg == 0) {
-      sm_m[pg][lane] = M;
-      sm_l[pg][lane] = L;
-    }
-#pragma unroll
-    for (int i = 0; i < DC; ++i) sm_o[pg][dg * DC + i][lane] = o[i];
-    __syncthreads();
-    // warp w sums up the dims [2 DG w, 2 DG (w + 1)) of every row
-    float k[PG], ref = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < PG; ++w) ref = fmaxf(ref, sm_m[w][lane]);
-    if (ref == -INFINITY) ref = 0.0f;
-    L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < PG; ++w) {
-      const float mw = sm_m[w][lane], lw = sm_l[w][lane];
-      k[w] = mw == -INFINITY ? (lw == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - ref);
-      L = fmaf(k[w], lw, L);
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint32_t y[DG];
-#pragma unroll
-    for (int j = 0; j < DG; ++j) {
-      float a = 0.0f, b = 0.0f;
-#pragma unroll
-      for (int w = 0; w < PG; ++w) {
-        a = fmaf(k[w], sm_o[w][2 * (DG * warp + j)][lane], a);
-        b = fmaf(k[w], sm_o[w][2 * (DG * warp + j) + 1][lane], b);
-      }
-      y[j] = pack_bf16x2(a * inv, b * inv);
-    }
-    if (live && d0 + 2 * DG * warp < D) {
-      uint32_t *to = reinterpret_cast<uint32_t *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D + d0) + DG * warp;
-      if constexpr (DG == 4) *reinterpret_cast<uint4 *>(to) = make_uint4(y[0], y[1], y[2], y[3]);
-      else to[0] = y[0];
-    }
-  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -935,11 +914,6 @@ bool map_3d(CUtensorMap *map, const void *base, int D, int64_t y, int64_t z, int
 // once for 256 rows), but for D = 256, whose accumulator fills tensor memory.
 int m_tiles(int D, int G, int N) { return D < 256 && N * G > kTile ? 2 : 1; }
 
-size_t desc_bytes() { return ((size_t)device_sm_count() * sizeof(TreeDesc) + 255) / 256 * 256; }
-
-// Blocks of 32 rows that a unit has at most.
-int merge_rows(const TreeAttnParams &p, int mt) { return (std::min(p.N * p.G, mt * kTile) + 31) / 32; }
-
 template <int D, int MT>
 cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
   auto kern = tree_attention_kernel<D, MT>;
@@ -953,33 +927,27 @@ cudaError_t launch(const TreeAttnParams &p, int ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  kern<<<ctas, TreeShape<D, MT>::THREADS, smem, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.by_unit ? p.by_unit : ctas), (unsigned)merge_rows(p, MT), (D + p.merge_dims - 1) / p.merge_dims);
-  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(TreeShape<D, MT>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeCooperative;  // CTAs wait for one another
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.merge_groups == 8 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, MT, 8>, p)
-                             : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, MT, 2>, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
 size_t tree_attention_scratch(int D, int G, int N) {
-  return desc_bytes() +
-         (size_t)device_sm_count() * kPartSlots * (size_t)(m_tiles(D, G, N) * kTile) * (D + 2) * sizeof(float);
+  return (size_t)device_sm_count() * kPartSlots * (size_t)(m_tiles(D, G, N) * kTile) * (D + 2) * sizeof(float);
 }
 
-cudaError_t launch_tree_attention(const TreeAttnParams &params, void *scratch, cudaStream_t s) {
+cudaError_t launch_tree_attention(const TreeAttnParams &params, cudaStream_t s) {
   TreeAttnParams p = params;
-  p.desc = static_cast<TreeDesc *>(scratch);
-  p.scratch = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + desc_bytes());
   const int mt = m_tiles(p.D, p.G, p.N);
   // the most tiles that there can be: all segments full
   int64_t most = 0;
@@ -996,14 +964,6 @@ cudaError_t launch_tree_attention(const TreeAttnParams &params, void *scratch, c
       !map_3d(&p.tq, p.q, p.D, p.Hq, (int64_t)p.B * p.N, p.G, kTile / p.G))
     return cudaErrorInvalidValue;
   const int sms = device_sm_count(), ctas = (int)(most < sms ? most : sms);
-  const int64_t units = (int64_t)p.B * p.Hkv * ((p.N * p.G + mt * kTile - 1) / (mt * kTile));
-  p.by_unit = units <= ctas ? (int)units : 0;
-  // the merge's blocks: as many as are resident at once (eight per SM), for few loads in a row
-  p.merge_groups = 2 * units >= ctas ? 2 : 8;
-  p.merge_dims = kMergeStep * kMergeWarps / p.merge_groups;
-  while (p.merge_dims < p.D &&
-         (int64_t)(p.by_unit ? p.by_unit : ctas) * merge_rows(p, mt) * (p.D / p.merge_dims) > 8 * sms)
-    p.merge_dims *= 2;
   if (p.D == 64) return mt == 2 ? launch<64, 2>(p, ctas, s) : launch<64, 1>(p, ctas, s);
   if (p.D == 128) return mt == 2 ? launch<128, 2>(p, ctas, s) : launch<128, 1>(p, ctas, s);
   return launch<256, 1>(p, ctas, s);

@@ -40,19 +40,34 @@ __device__ __forceinline__ Ask ask_of(const BlockTablesParams &p, int b, int *ba
   return a;
 }
 
-// Slots of sequence b's next tokens: entries first, first + step, ... of its row.
+// Slots of sequence b's next tokens: W of its row's entries at a time, first, first + step, ....
+template <int W>
 __device__ __forceinline__ void map_row(const BlockTablesParams &p, int b, int32_t len, int32_t n,
                                         bool served, int first, int step) {
   const int32_t *row = p.table + (int64_t)b * p.max_blocks;
   int32_t *to = p.slot_map + (int64_t)b * p.max_new;
-  for (int i = first; i < p.max_new; i += step) {
-    int32_t slot = -1;
-    if (served && i < n) {
-      const int32_t t = len + i;
-      slot = (row[t >> p.shift] << p.shift) + (t & ((1 << p.shift) - 1));
+  const bool whole = W == 4 && p.max_new % 4 == 0 && (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0;
+  for (int i = W * first; i < p.max_new; i += W * step) {
+    int32_t slot[4];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const int32_t t = len + i + k;
+      slot[k] = served && i + k < n ? (row[t >> p.shift] << p.shift) + (t & ((1 << p.shift) - 1)) : -1;
     }
-    to[i] = slot;
+    if (W == 4 && whole) {
+      *reinterpret_cast<int4 *>(to + i) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k)
+        if (i + k < p.max_new) to[i + k] = slot[k];
+    }
   }
+}
+
+// Place `at` of the ring (at < 3 n: the head, the free blocks and those that change hands).
+__device__ __forceinline__ int32_t ring_place(int32_t at, int32_t n) {
+  at = at >= n ? at - n : at;
+  return at >= n ? at - n : at;
 }
 
 // Inclusive prefix sums of two values over the block's first 256 threads.
@@ -144,21 +159,40 @@ __global__ void __launch_bounds__(kTableThreads)
     const int32_t n0 = s_new[b], n1 = s_old[b];
     if (n1 <= n0) continue;
     int32_t *row = p.table + (int64_t)b * p.max_blocks;
-    for (int j = n0 + first; j < n1; j += step) {
-      const int64_t at = (int64_t)head + count + s_rel[b] + (j - n0);
-      p.ring[at % p.n_blocks] = row[j];
-      row[j] = -1;
+    for (int j0 = n0 + first; j0 < n1; j0 += 4 * step) {  // four loads under way
+      int32_t id[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j0 + k * step < n1) id[k] = row[j0 + k * step];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + k * step;
+        if (j < n1) {
+          p.ring[ring_place(head + count + s_rel[b] + (j - n0), p.n_blocks)] = id[k];
+          row[j] = -1;
+        }
+      }
     }
   }
   sync();  // what was released can be taken, and every CTA has read the counts and the ring's state
   for (int b = group; b < p.B; b += groups) {
     const int32_t n0 = s_old[b], n1 = s_new[b];
     int32_t *row = p.table + (int64_t)b * p.max_blocks;
-    for (int j = n0 + first; j < n1; j += step) {
-      const int64_t at = (int64_t)head + s_take[b] + (j - n0);
-      const int32_t id = p.ring[at % p.n_blocks];
-      if (id < 0 || id >= p.n_blocks) dev::set_error(p.err, TRIA_DEVERR_PAGES);
-      row[j] = id;
+    for (int j0 = n0 + first; j0 < n1; j0 += 4 * step) {
+      int32_t id[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + k * step;
+        if (j < n1) id[k] = p.ring[ring_place(head + s_take[b] + (j - n0), p.n_blocks)];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + k * step;
+        if (j < n1) {
+          if (id[k] < 0 || id[k] >= p.n_blocks) dev::set_error(p.err, TRIA_DEVERR_PAGES);
+          row[j] = id[k];
+        }
+      }
     }
   }
   if (rank == 0 && tid < p.B) p.held[tid] = s_new[tid];
@@ -173,7 +207,7 @@ __global__ void __launch_bounds__(kTableThreads)
   }
   if (!map_inline) return;
   sync();  // the rows are complete
-  for (int b = group; b < p.B; b += groups) map_row(p, b, s_len[b], s_n[b], s_n[b] >= 0, first, step);
+  for (int b = group; b < p.B; b += groups) map_row<1>(p, b, s_len[b], s_n[b], s_n[b] >= 0, first, step);
 }
 
 __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const __grid_constant__ BlockTablesParams p) {
@@ -184,7 +218,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const __grid_cons
   const int32_t held = p.held[b];
   const bool served = a.ok && held >= 0 && held <= p.max_blocks &&
                       (int64_t)a.len + a.n <= ((int64_t)held << p.shift);
-  map_row(p, b, a.len, a.n, served, blockIdx.x * kMapThreads + threadIdx.x, gridDim.x * kMapThreads);
+  map_row<4>(p, b, a.len, a.n, served, blockIdx.x * kMapThreads + threadIdx.x, gridDim.x * kMapThreads);
 }
 
 }  // namespace
@@ -206,7 +240,7 @@ cudaError_t launch_block_tables(const BlockTablesParams &p, cudaStream_t s) {
   const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, block_tables_kernel<kTableCluster>, p, small ? 1 : 0)
                              : cudaLaunchKernelEx(&cfg, block_tables_kernel<1>, p, small ? 1 : 0);
   if (e != cudaSuccess || small) return e;
-  const int64_t per = ((int64_t)p.max_new + kMapThreads - 1) / kMapThreads;
+  const int64_t per = ((int64_t)p.max_new + 4 * kMapThreads - 1) / (4 * kMapThreads);
   cfg.gridDim = dim3((unsigned)(per < 1024 ? per : 1024), (unsigned)p.B, 1);
   cfg.blockDim = dim3(kMapThreads, 1, 1);
   attr[0] = {};

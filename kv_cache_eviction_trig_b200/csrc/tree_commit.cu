@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(kCommitThreads)
     tree_commit_kernel(const __grid_constant__ TreeCommitParams p) {
   __shared__ int32_t parent[TRIA_MAX_NODES];
   __shared__ int32_t path[TRIA_MAX_NODES];  // leaf first
+  __shared__ int32_t slots[TRIA_MAX_NODES];
   __shared__ int32_t depth;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t rows = (int64_t)p.L * p.Hkv;
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(kCommitThreads)
     for (int j = tid; j < len && j < p.max_new; j += kCommitThreads) {
       const int32_t s = p.slot_map[(int64_t)b * p.max_new + j];
       if (s < 0 || (int64_t)s >= p.cap) bad |= TRIA_DEVERR_PAGES;
+      slots[j] = s;
     }
   }
   if (__syncthreads_or(bad)) {
@@ -77,15 +79,30 @@ __global__ void __launch_bounds__(kCommitThreads)
     const uint4 *vs = reinterpret_cast<const uint4 *>(p.v_new) + (lg * p.B + b) * p.N * nv;
     uint4 *kd = reinterpret_cast<uint4 *>(p.k) + lg * p.cap * nv;
     uint4 *vd = reinterpret_cast<uint4 *>(p.v) + lg * p.cap * nv;
-    for (int j = 0; j < len; ++j) {
-      const int64_t slot = p.slot_map ? p.slot_map[(int64_t)b * p.max_new + j] : T + j;
-      const int64_t node = path[len - 1 - j];
-      for (int i = lane; i < 2 * nv; i += 32) {
-        if (i < nv) kd[slot * nv + i] = ks[node * nv + i];
-        else vd[slot * nv + i - nv] = vs[node * nv + i - nv];
+    // the path's 16-byte vectors, K's of a row before V's, four per lane under way
+    const int row_vecs = 2 * nv, vecs = len * row_vecs;
+    auto slot_of = [&](int j) { return p.slot_map ? (int64_t)slots[j] : T + j; };
+    for (int i0 = lane; i0 < vecs; i0 += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + 32 * k, j = i / row_vecs, e = i - j * row_vecs;
+        if (i < vecs) {
+          const int64_t node = path[len - 1 - j];
+          v[k] = e < nv ? ks[node * nv + e] : vs[node * nv + e - nv];
+        }
       }
-      if (lane == 0) p.pos[lg * p.cap + slot] = cur + 1 + j;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + 32 * k, j = i / row_vecs, e = i - j * row_vecs;
+        if (i < vecs) {
+          const int64_t slot = slot_of(j);
+          if (e < nv) kd[slot * nv + e] = v[k];
+          else vd[slot * nv + e - nv] = v[k];
+        }
+      }
     }
+    for (int j = lane; j < len; j += 32) p.pos[lg * p.cap + slot_of(j)] = cur + 1 + j;
   }
   // the sequence's last block advances its lengths: the others have read them
   __syncthreads();

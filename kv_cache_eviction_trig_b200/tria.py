@@ -167,8 +167,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the handle alone: a Stream object takes 3 us to make, as long as a launch
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 class Config:
@@ -364,6 +366,12 @@ def tria_decode_attention(cfg: Config, cache: Cache, layer: int, q: torch.Tensor
                                        ws.numel(), _stream(stream)), "tria_decode_attention")
 
 
+def _check_device(t: torch.Tensor):
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {t.get_device()}, the current one is "
+                         f"{torch.cuda.current_device()}")
+
+
 def _check_tree(cfg: Config, tree: Tree):
     c = cfg.c
     want = (c.num_layers, c.n_kv_heads, c.batch, tree.c.max_nodes, c.head_dim)
@@ -377,6 +385,7 @@ def tria_tree_attention(cfg: Config, cache: Cache, tree: Tree, layer: int, q: to
     """q, out: bf16 [B][N][Hq][D] device tensors; rows past a sequence's nodes are neither
     read nor written; scale None (or <= 0) lets the library use 1/sqrt(D)."""
     _check_tree(cfg, tree)
+    _check_device(q)
     rows = (cfg.c.batch, tree.c.max_nodes, cfg.c.n_q_heads, cfg.c.head_dim)
     _check(lib().tria_tree_attention(
         ctypes.byref(cfg.c), ctypes.byref(cache.c), ctypes.byref(tree.c), layer,
@@ -390,6 +399,7 @@ def tria_tree_commit(cfg: Config, cache: Cache, tree: Tree, last: torch.Tensor, 
     """last: int32 [B], each sequence's last accepted node or -1; slot_map: int32 [B][max_new]
     as tria_block_tables wrote it, for a paged cache."""
     _check_tree(cfg, tree)
+    _check_device(last)
     B = cfg.c.batch
     max_new = 0 if slot_map is None else slot_map.shape[1]
     _check(lib().tria_tree_commit(
@@ -403,6 +413,7 @@ def tria_block_tables(cfg: Config, cache: Cache, n_new: torch.Tensor,
                       slot_map: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
     """n_new: int32 [B], the tokens each sequence is about to add; slot_map: int32
     [B][max_new], or None to update the tables alone (n_new is then all 0)."""
+    _check_device(n_new)
     B = cfg.c.batch
     max_new = 0 if slot_map is None else slot_map.shape[1]
     _check(lib().tria_block_tables(

@@ -27,9 +27,9 @@
 // cooperative: all CTAs are resident, and each reports its parts before it waits.  A merge
 // kernel of its own took 7 us from the last part to the last row, this one 2 us.)
 //
-// Rounding: S, maxima, sums and O are float32.  P multiplies the bf16 V as a bf16 pair high +
-// low (16 significant bits), so that the output's rounding to bf16 is the only one that
-// counts; with the high halves alone the error is 1.4 to 1.6 times that.
+// Rounding: S, maxima, sums and O are float32.  P is rounded to bf16 for the product with
+// the bf16 V (its error is that of the bf16 output's own rounding); the sum is of the
+// unrounded P.
 //
 // Masks.  Columns past the length, and nodes off a row's path, are set to -inf in S.  V rows
 // past the length are zeroed in shared memory (P is 0 there, but 0 * NaN is not), and
@@ -89,7 +89,6 @@ struct TreeCtl {
   float swap[2][2][2][kTile];          // what a row's two threads exchange: in turn, by M tile and half
   uint32_t tn[TRIA_MAX_BATCH];         // live length (0 with per-unit lengths) << 9 | nodes (0: skipped)
   int16_t parent[TRIA_MAX_NODES];
-  TreePart todo[2];                    // the units of which this CTA has a part
 };
 static_assert(TRIA_MAX_NODES < 512 && TRIA_MAX_SEGMENT < (1 << 23), "lengths and nodes in one word");
 
@@ -136,15 +135,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // Two float32 products and sums at a time.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-
-// Two floats as bf16 pairs high + low: the upper halves of their bits, and the rest rounded.
-__device__ __forceinline__ void split_bf16(float2 a, uint32_t &hi, uint32_t &lo) {
-  const uint32_t x = __float_as_uint(a.x), y = __float_as_uint(a.y);
-  hi = __byte_perm(x, y, 0x7632);
-  const float2 top = make_float2(-__uint_as_float(x & 0xffff0000u), -__uint_as_float(y & 0xffff0000u));
-  const float2 rest = add2(a, top);
-  lo = pack_bf16x2(rest.x, rest.y);
-}
 
 // The tiles [k0, k1) of unit (b, g, mg), which has K tiles, KT of them cached.
 struct Piece {
@@ -515,10 +505,8 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       const int s = v_seq<MT>(x, X) % NS, buf = MT == 2 ? m : x & 1;
       const uint64_t vd = tc::desc(base_lo + S::OFF_RING + s * TB, SLAB);
 #pragma unroll
-      for (int k = 0; k < 2 * (kTile / 16); ++k) {  // of 32 keys two steps for the high halves, two for the low
-        const int key = 2 * (k >> 2) + (k & 1);       // 16 keys each
-        tc::mma_ts(tm_o[m], tm_s[buf] + 8 * k, vd + (2048 >> 4) * key, tc::instr(D, true), !first || k > 0, one);
-      }
+      for (int k = 0; k < kTile / 16; ++k)
+        tc::mma_ts(tm_o[m], tm_s[buf] + 8 * k, vd + (2048 >> 4) * k, tc::instr(D, true), !first || k > 0, one);
       tc::commit(&c.o_full[m], one);
       if (m == MT - 1) tc::commit(&c.empty[s], one);
     };
@@ -585,6 +573,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     // the units of which this CTA has a part: what their merge needs
     constexpr int ROWS = MT * kTile;
     int pending = 0;
+    TreePart todo[2];
     // The products with V up to that of tile x - 1 have completed.  (A parity tells only the
     // last two phases of a barrier apart.  While this row's P of tile x is outstanding, that of
     // x - 1 or x - 2 is the last that can have completed, as S of x came after x - 2.)
@@ -606,7 +595,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         }
       }
       float mr = -INFINITY, l = 0.0f;
-      bool hurt = false;  // the V of a node on this row's path has Inf or NaN
+      uint32_t hurt[2][4] = {};  // nodes on this row's path whose V has Inf or NaN
       for (int kt = u.k0; kt < u.k1; ++kt, ++x) {
         const int buf = MT == 2 ? m : x & 1;
         const bool draft = kt >= u.KT;
@@ -678,28 +667,34 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
             }
             mr = ceilf(sl * both(fmaxf(mx[0], mx[1])));
           }
-          // P with the maximum so far, which as a rule stands (within 2^8), 32 keys at a time;
+          // P with the maximum so far, which as a rule stands (within 2^8), 64 keys at a time;
           // if theirs is larger, once more with that.  Maxima are rounded up to whole powers
           // of two, so that a change of scale is exact.
 #pragma unroll 1
-          for (int e = 0; e < HK / 32; ++e) {
+          for (int h = 0; h < HK / 64; ++h) {
             float2 sum;
-            uint32_t w[32];  // high halves, low halves
+            uint32_t w[32];
             for (;;) {
               const float base = mr == -INFINITY ? 0.0f : mr;
               const float2 scale2 = make_float2(sl, sl), base2 = make_float2(-base, -base);
               float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-              float mx[2] = {-INFINITY, -INFINITY}, s[32];
-              ask(e, s);
+              float mx[2] = {-INFINITY, -INFINITY};
+              float s[2][32];
+              ask(2 * h, s[0]);
               tc::wait_ld();
+              ask(2 * h + 1, s[1]);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 y = fma2(make_float2(s[2 * i], s[2 * i + 1]), scale2, base2);
-                mx[0] = fmaxf(mx[0], y.x);
-                mx[1] = fmaxf(mx[1], y.y);
-                const float2 a = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                sums[i & 1] = add2(sums[i & 1], a);
-                split_bf16(a, w[i], w[16 + i]);
+              for (int e = 0; e < 2; ++e) {
+                if (e == 1) tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 y = fma2(make_float2(s[e][2 * i], s[e][2 * i + 1]), scale2, base2);
+                  mx[0] = fmaxf(mx[0], y.x);
+                  mx[1] = fmaxf(mx[1], y.y);
+                  const float2 a = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                  sums[i & 1] = add2(sums[i & 1], a);
+                  w[16 * e + i] = pack_bf16x2(a.x, a.y);
+                }
               }
               sum = add2(sums[0], sums[1]);
               const float mn = fmaxf(mr, ceilf(base + both(fmaxf(mx[0], mx[1]))));
@@ -718,21 +713,21 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
                   tc::st32(tm_o[m] + lane_off + d, o);
                 }
               }
-#pragma unroll 1
-              for (int k = 0; k < e; ++k) {  // and the tile's P so far
+              if (h > 0) {  // and the tile's first half of P
                 uint32_t o[32];
                 tc::wait_st();
-                tc::ld32(ts + half * HK + 32 * k, o);
+                tc::ld32(ts, o);
                 tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = pack_bf16x2(dev::bf16lo(o[i]) * a, dev::bf16hi(o[i]) * a);
-                tc::st32(ts + half * HK + 32 * k, o);
+                tc::st32(ts, o);
               }
               l *= a;
               mr = mn;
             }
             l += sum.x + sum.y;
-            tc::st32(ts + half * HK + 32 * e, w);  // over the S of the same keys
+            // (both threads of the row have read the S that this overwrites)
+            tc::st32(ts + (HK / 2) * half + 32 * h, w);
           }
         }
         if (masked) {
@@ -772,7 +767,10 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             dev::named_barrier(1, ALL);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hurt |= (on[e] & c.poison[e]) != 0;
+            for (int e = 0; e < 4; ++e) {
+              if (kt > u.KT) hurt[1][e] = on[e] & c.poison[e];
+              else hurt[0][e] = on[e] & c.poison[e];
+            }
           } else {
             for (int i = part_id; i < (kTile - valid) * (D / 8); i += 128 * NH) {
               const int r = valid + i / (D / 8), q = i % (D / 8);
@@ -803,26 +801,26 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint4 *to = reinterpret_cast<uint4 *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D);
         float *part = p.scratch + ((size_t)cta * kPartSlots + (u.k0 > 0 ? 0 : 1)) * (size_t)(MT * kTile) * (D + 2) + r;
+        bool any_hurt = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any_hurt |= (hurt[0][e] | hurt[1][e]) != 0;
 #pragma unroll 1
         for (int d = half * HD; d < (half + 1) * HD; d += 32) {
           float o[32];
           __syncwarp();
           tc::ld32(tm_o[m] + lane_off + d, reinterpret_cast<uint32_t *>(o));
           tc::wait_ld();
-          if (hurt) {  // (of the path's nodes that this piece has seen)
-            const int lo = max(0, u.k0 - u.KT) * kTile, end = (u.k1 - u.KT) * kTile;
-            for (int j = node; j >= lo; j = c.parent[j]) {
-              const uint16_t *v = p.vd + ((((int64_t)p.layer * p.Hkv + u.g) * p.B + u.b) * p.N + j) * D + d;
-              if (j < end)
-#pragma unroll 1
+          if (any_hurt) {
+            for (int e = 0; e < 8; ++e)
+              for (uint32_t bits = hurt[e >> 2][e & 3]; bits; bits &= bits - 1) {
+                const int j = 32 * e + __ffs(bits) - 1;
+                const uint16_t *v = p.vd + ((((int64_t)p.layer * p.Hkv + u.g) * p.B + u.b) * p.N + j) * D + d;
+#pragma unroll
                 for (int i = 0; i < 32; ++i) {
                   const float f = __uint_as_float((uint32_t)v[i] << 16);
-                  if (!isfinite(f)) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] += k == i ? f : 0.0f;
-                  }
+                  if (!isfinite(f)) o[i] += f;
                 }
-            }
+              }
           }
           if (live && whole) {
 #pragma unroll
@@ -845,15 +843,13 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       dev::mbar_arrive(&c.o_free[m]);
       if (!whole) {  // reported once all threads have stored it
         const int64_t from = (int64_t)w0 + x - (u.k1 - u.k0) - u.k0, to = from + u.K;  // the unit's tiles
-        TreePart t;
+        TreePart &t = todo[pending++];
         t.b = u.b;
         t.head0 = u.g * p.G;
         t.node0 = u.mg * MT * per;
         t.n = u.n;
         t.first = (int32_t)(((from + 1) * ctas + total - 1) / total) - 1;
         t.last = (int32_t)((to * ctas + total - 1) / total) - 1;
-        if (kid == 0) c.todo[pending] = t;
-        ++pending;
         __threadfence();
         dev::named_barrier(1, ALL);
         if (kid == 0) atomicAdd(p.arrived + t.first * kArriveStride, 1);
@@ -861,7 +857,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     }
     // ---------------------------------------------------------------- merge
     for (int k = 0; k < pending; ++k) {
-      const TreePart t = c.todo[k];
+      const TreePart t = todo[k];
       const int parts = t.last - t.first + 1;
       int32_t *arrived = p.arrived + t.first * kArriveStride;
       if (kid == 0) {

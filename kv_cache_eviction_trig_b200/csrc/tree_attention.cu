@@ -90,7 +90,8 @@ struct TreeCtl {
   uint32_t poison[4];                  // drafted V rows of the tile with Inf or NaN
   float swap[2][2][2][kTile];          // what a row's two threads exchange: in turn, by M tile and half
   uint32_t tn[TRIA_MAX_BATCH];         // live length (0 with per-unit lengths) << 9 | nodes (0: skipped)
-  int16_t parent[TRIA_MAX_NODES];
+  uint32_t path[TRIA_MAX_NODES / 32][TRIA_MAX_NODES];  // word w of the node's path
+  int16_t jump[TRIA_MAX_NODES];
 };
 static_assert(TRIA_MAX_NODES < 512 && TRIA_MAX_SEGMENT < (1 << 23), "lengths and nodes in one word");
 
@@ -126,6 +127,18 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int32_t 
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dev::smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(dev::smem_addr(bar))
       : "memory");
+}
+
+// A named barrier that tells whether any of its threads gave true.
+__device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t threads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"((uint32_t)mine)
+      : "memory");
+  return any != 0;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -605,20 +618,39 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
         const bool masked = draft || valid < kTile;
         uint32_t on[4] = {~0u, ~0u, ~0u, ~0u};  // the tile's columns that this row sees
         if (draft) {
-          dev::named_barrier(1, ALL);  // the last tile's parents and marks have been read
+          constexpr int PW = TRIA_MAX_NODES / 32;
+          dev::named_barrier(1, ALL);  // the last tile's paths and marks have been read
           if (kid < 4) c.poison[kid] = 0;
-          if (kid < TRIA_MAX_NODES) c.parent[kid] = (int16_t)up;
-          dev::named_barrier(1, ALL);
-          const int j0 = (kt - u.KT) * kTile;
+          if (kt == max(u.KT, u.k0)) {
+            // Every node's path as bits, once per piece, a thread per node, by doubling: what
+            // its path is known to hold joins what that of the node `to` holds, the first one
+            // not known yet, and `to` moves on to that node's.
+            uint32_t bits[PW];
+            int to = up;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) on[e] = 0u;
-          if (live)
-            for (int j = node; j >= j0; j = c.parent[j]) {
-              const int q = j - j0;
+            for (int w = 0; w < PW; ++w) c.path[w][kid] = bits[w] = w == kid >> 5 ? 1u << (kid & 31) : 0u;
+            c.jump[kid] = (int16_t)to;
+            dev::named_barrier(1, ALL);
+            for (;;) {
+              uint32_t more[PW];
+              int next = -1;
+              if (to >= 0) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((q >> 5) == e) on[e] |= 1u << (q & 31);
+                for (int w = 0; w < PW; ++w) more[w] = c.path[w][to];
+                next = c.jump[to];
+              }
+              if (!barrier_any(1, ALL, to >= 0)) break;  // (and all have read)
+              if (to >= 0) {
+#pragma unroll
+                for (int w = 0; w < PW; ++w) c.path[w][kid] = bits[w] |= more[w];
+                c.jump[kid] = (int16_t)(to = next);
+              }
+              dev::named_barrier(1, ALL);
             }
+          }
+          dev::named_barrier(1, ALL);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) on[e] = live ? c.path[(kt - u.KT) * (kTile / 32) + e][node] : 0u;
         } else if (masked) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)

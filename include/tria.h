@@ -341,9 +341,9 @@ tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,
                              int32_t max_new, void *ws, size_t ws_bytes, void *stream);
 
 /* Brings a paged cache's block tables up to date with the lengths on the GPU, and maps the
- * next tokens to slots (dimensionstp.github.io review, section 6, Limitations: the pruned
- * cache in a paged KV cache; a prune shortens sequences on the device, so the host does not
- * know which blocks they still need).  n_new is DEVICE int32 [B], the tokens that sequence b
+ * next tokens to slots (dimensionstp.github.io review, section 6, Limitations: serving with a
+ * paged KV cache; the accepted paths grow the lengths on the device, so the host does not
+ * know which blocks the sequences need; a length of 0 ends one).  n_new is DEVICE int32 [B], the tokens that sequence b
  * is about to add, each in [0, max_new].  With need = ceil((seq_len[b] + n_new[b]) /
  * block_size) blocks for sequence b:
  *   - blocks past the need go back to the pool's tail, in the order of (b, place);

@@ -718,7 +718,8 @@ tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
   tp.scratch = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsPrefix);
   // the counters live in the workspace's zero-at-rest prefix
   tp.arrived = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsHist);
-  return cuda_status(launch_tree_attention(tp, static_cast<cudaStream_t>(stream)));
+  const cudaError_t e = launch_tree_attention(tp, static_cast<cudaStream_t>(stream));
+  return e == cudaErrorNotSupported ? TRIA_ERR_UNSUPPORTED : cuda_status(e);
 }
 
 tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,

@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       int32_t *arrived = p.arrived + t.first * kArriveStride;
       if (kid == 0) {
         int32_t seen = 0;
-        for (uint32_t i = 0; i < 20000000u && seen < parts; ++i) {
+        for (uint32_t i = 0; i < 3000000u && seen < parts; ++i) {
           asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(arrived) : "memory");
           if (*reinterpret_cast<volatile int32_t *>(&c.abort)) break;
         }
@@ -937,7 +937,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 bool map_3d(CUtensorMap *map, const void *base, int D, int64_t y, int64_t z, int by, int bz) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)(y > 0 ? y : 1), (cuuint64_t)z};  // (an empty cache is not read)
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * (cuuint64_t)y};
   const cuuint32_t box[3] = {64, (cuuint32_t)by, (cuuint32_t)bz};
   const cuuint32_t estr[3] = {1, 1, 1};
@@ -991,7 +991,8 @@ cudaError_t launch_tree_attention(const TreeAttnParams &params, cudaStream_t s) 
     most += (p.seg_start[b + 1] - p.seg_start[b] + kTile - 1) / kTile + (p.N + kTile - 1) / kTile;
   most *= (int64_t)p.Hkv * ((p.N * p.G + mt * kTile - 1) / (mt * kTile));
   const int64_t heads = (int64_t)p.L * p.Hkv;
-  if (most > INT32_MAX || p.cap > INT32_MAX || heads * p.B > INT32_MAX) return cudaErrorInvalidValue;
+  if (most > INT32_MAX || p.cap > INT32_MAX || heads * p.B > INT32_MAX) return cudaErrorNotSupported;
+  if (most == 0) return cudaSuccess;
   p.draft_rows = p.N < kTile ? p.N : kTile;
   const int rows = p.pages.table && p.pages.shift < 7 ? 1 << p.pages.shift : kTile;
   if (!map_3d(&p.tk, p.k, p.D, p.cap, heads, rows, 1) || !map_3d(&p.tv, p.v, p.D, p.cap, heads, rows, 1) ||

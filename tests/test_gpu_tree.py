@@ -540,3 +540,256 @@ def test_block_tables_refuse_a_corrupt_pool():
             assert slots[0, :3].tolist() == [3, 4, -1]   # it holds the block of these tokens
         else:  # the other sequence is served
             assert pages.tensors[1].tolist() == [1, 5] and pages.tensors[3].tolist() == [0, 6]
+
+
+# ---------------------------------------------------------------- the calls together
+
+def _draw_trees(rng, L, Hkv, B, N, D):
+    f = lambda *s: torch.tensor(rng.normal(size=s), dtype=torch.float32).to(torch.bfloat16)
+    nodes = rng.integers(0, N + 1, B)
+    return dict(parent=torch.tensor(_parents("tree", B, N, rng), dtype=torch.int32),
+                n_nodes=torch.tensor(nodes, dtype=torch.int32), kd=f(L, Hkv, B, N, D),
+                vd=f(L, Hkv, B, N, D),
+                last=torch.tensor([rng.integers(-1, n) if n else -1 for n in nodes], dtype=torch.int32))
+
+
+def test_speculative_loop_over_pages_matches_oracle_and_its_graph():
+    """Twelve steps of: blocks for a tree's tokens, the trees' attention in every layer, the
+    accepted paths into the cache; requests end and start in between.  The first steps run
+    eagerly, the others from one captured graph."""
+    L, Hkv, Hq, D, B, N, block, steps = 2, 2, 4, 64, 3, 10, 16, 12
+    rng = np.random.default_rng(5)
+    caps, n_blocks = [160, 96, 160], 20          # 26 blocks would hold them all
+    starts = np.concatenate([[0], np.cumsum(caps)]).tolist()
+    bf, i32 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.int32, device="cuda")
+    cap = n_blocks * block
+    t = dict(k=torch.full((L, Hkv, cap, D), float("nan"), **bf), v=torch.full((L, Hkv, cap, D), float("nan"), **bf),
+             pos=torch.zeros(L, Hkv, cap, **i32), seq_len=torch.zeros(B, **i32), cur_pos=torch.zeros(B, **i32),
+             parent=torch.zeros(B, N, **i32), n_nodes=torch.zeros(B, **i32), last=torch.zeros(B, **i32),
+             n_new=torch.zeros(B, **i32), slots=torch.zeros(B, N, **i32),
+             kd=torch.zeros(L, Hkv, B, N, D, **bf), vd=torch.zeros(L, Hkv, B, N, D, **bf),
+             q=torch.zeros(L, B, N, Hq, D, **bf), out=torch.zeros(L, B, N, Hq, D, **bf))
+    pages = tria.Pages.empty(B, max(caps) // block, n_blocks, block)
+    cfg = tria.Config(num_layers=L, batch=B, n_q_heads=Hq, n_kv_heads=Hkv, head_dim=D,
+                      rope_theta=1e6, budget=64, offsets=[1])
+    cache = tria.Cache(t["k"], t["v"], t["pos"], t["seq_len"], t["cur_pos"], starts, pages=pages)
+    tree = tria.Tree(t["parent"], t["n_nodes"], t["kd"], t["vd"])
+    ws = tria.workspace(cfg, cache, tree=tree)
+
+    def step():
+        tria.tria_block_tables(cfg, cache, t["n_new"], t["slots"], ws)
+        for layer in range(L):
+            tria.tria_tree_attention(cfg, cache, tree, layer, t["q"][layer], t["out"][layer], ws)
+        tria.tria_tree_commit(cfg, cache, tree, t["last"], ws, slot_map=t["slots"])
+
+    state = [x.cpu().numpy() for x in pages.tensors]
+    graph, lens, cur, served = None, [0, 0, 0], [0, 0, 0], 0
+    kept = {(b, l, g): [] for b in range(B) for l in range(L) for g in range(Hkv)}   # (k, v) rows
+    for n in range(steps):
+        if n in (5, 9):                          # a request ends, a new one takes its place
+            lens[n % B], cur[n % B] = 0, 0
+            t["seq_len"][n % B], t["cur_pos"][n % B] = 0, 0
+            for l in range(L):
+                for g in range(Hkv):
+                    kept[n % B, l, g] = []
+        d = _draw_trees(rng, L, Hkv, B, N, D)
+        q = torch.tensor(rng.normal(size=(L, B, N, Hq, D)), dtype=torch.float32).to(torch.bfloat16)
+        for name, x in (*d.items(), ("q", q)):
+            t[name].copy_(x)
+        t["n_new"].copy_(d["n_nodes"])
+        t["out"].fill_(7.0)
+        if graph is None and n >= 3:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        tria.tria_workspace_init(ws)
+        graph.replay() if graph is not None else step()
+        torch.cuda.synchronize()
+        want = oracle.block_tables(*state, block, lens, d["n_nodes"].tolist(), caps, N)
+        state = [np.asarray(x) for x in want[:4]]
+        for got, ref in zip(pages.tensors, state):
+            assert np.array_equal(got.cpu().numpy(), ref)
+        assert np.array_equal(t["slots"].cpu().numpy(), want[4])
+        # the attention, from the rows that were committed so far
+        nodes, parent = d["n_nodes"].tolist(), d["parent"].numpy()
+        for l in range(L):
+            k = torch.zeros(1, Hkv, sum(lens) + 1, D, dtype=torch.bfloat16)
+            v, at, slots = torch.zeros_like(k), 0, []
+            for b in range(B):
+                for g in range(Hkv):
+                    for j, (kr, vr) in enumerate(kept[b, l, g]):
+                        k[0, g, at + j], v[0, g, at + j] = kr, vr
+                slots.append([np.arange(at, at + lens[b])] * Hkv)
+                at += lens[b]
+            ref, spread, steep = oracle.tree_attention(
+                common.bf16_bits(k), common.bf16_bits(v), slots, common.bf16_bits(d["kd"][l:l + 1]),
+                common.bf16_bits(d["vd"][l:l + 1]), parent, nodes, common.bf16_bits(q[l]), 0, D ** -0.5)
+            got = t["out"][l].double().cpu().numpy()
+            for b in range(B):
+                m = nodes[b]
+                assert np.all(got[b, m:] == 7.0)
+                logit = 2 * D * 2.0 ** -23 * steep[b, :m, :, None]
+                tol = 2.0 ** -8 * np.abs(ref[b, :m]) + (2.0 ** -8 + logit + 2.0 ** -16) * spread[b, :m]
+                assert np.all(np.abs(got[b, :m] - ref[b, :m]) <= tol), (n, l, b)
+        # the commit
+        code = 0
+        for b in range(B):
+            path = oracle.tree_path(parent[b], int(d["last"][b]))
+            if b in want[5]:
+                code |= {"pool": tria.DEVERR_POOL, "full": tria.DEVERR_SEGMENT_FULL}[want[5][b]]
+                if path:
+                    code |= tria.DEVERR_SEGMENT_FULL if lens[b] + len(path) > caps[b] else 0
+                    code |= tria.DEVERR_PAGES    # its slots are -1
+                continue
+            served += len(path)
+            for l in range(L):
+                for g in range(Hkv):
+                    for j, node in enumerate(path):
+                        kept[b, l, g].append((d["kd"][l, g, b, node], d["vd"][l, g, b, node]))
+                        assert int(t["pos"][l, g, want[4][b, j]]) == cur[b] + 1 + j
+            lens[b] += len(path)
+            cur[b] += len(path)
+        assert tria.tria_get_device_error(ws) == code, n
+        assert t["seq_len"].tolist() == lens and t["cur_pos"].tolist() == cur
+    assert served > 40
+    del graph
+
+
+def test_speculative_loop_with_the_windowed_prune():
+    """Segments: trees of drafted tokens, accepted paths, and the prune back to the budget once
+    a window of them has joined; every step against the oracle run from the state before it."""
+    from tests.test_gpu_decode import _check_windowed, _problem, _state
+    from tests.test_gpu_parity import Case, small
+    budget, W, N, steps = 48, 16, 9, 14
+    wl = small("speculative", L=2, B=3, Hq=4, Hkv=2, D=64, theta=1e4, seq_lens=[40, 60, 63],
+               budget=budget, slack=40, offsets=range(1, 33))
+    a = Case(wl)
+    cfg = tria.Config.from_workload(wl, prune_window=W)
+    rng = np.random.default_rng(8)
+    L, Hkv, B, D = 2, 2, 3, 64
+    d = _draw_trees(rng, L, Hkv, B, N, D)
+    t = {n: x.cuda() for n, x in d.items()}
+    tree = tria.Tree(t["parent"], t["n_nodes"], t["kd"], t["vd"])
+    ws = tria.workspace(cfg, a.cache, tree=tree)
+    q, out = torch.zeros(B, N, 4, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, N, 4, D, dtype=torch.bfloat16, device="cuda")
+    sel = torch.empty((L, Hkv, B, budget), dtype=torch.int32, device="cuda")
+    pruned = 0
+    for _ in range(steps):
+        d = _draw_trees(rng, L, Hkv, B, N, D)
+        for n, x in d.items():
+            t[n].copy_(x)
+        q.copy_(torch.tensor(rng.normal(size=q.shape), dtype=torch.float32))
+        before = _state(a)
+        sel.fill_(-7)
+        tria.tria_tree_attention(cfg, a.cache, tree, 1, q, out, ws)
+        tria.tria_tree_commit(cfg, a.cache, tree, t["last"], ws)
+        torch.cuda.synchronize()
+        joined = _state(a)
+        tria.tria_prune(cfg, a.stats, a.cache, ws, sel_out=sel)
+        torch.cuda.synchronize()
+        assert tria.tria_get_device_error(ws) == 0
+        # attention over the keys before the step
+        starts = a.host["seq_start"]
+        slots = [[starts[b] + np.arange(before["seq_len"][b])] * Hkv for b in range(B)]
+        ref, spread, steep = oracle.tree_attention(
+            before["k"], before["v"], slots, common.bf16_bits(d["kd"]), common.bf16_bits(d["vd"]),
+            d["parent"].numpy(), d["n_nodes"].tolist(), common.bf16_bits(q), 1, D ** -0.5)
+        got = out.double().cpu().numpy()
+        for b in range(B):
+            m = int(d["n_nodes"][b])
+            logit = 2 * D * 2.0 ** -23 * steep[b, :m, :, None]
+            tol = 2.0 ** -8 * np.abs(ref[b, :m]) + (2.0 ** -8 + logit + 2.0 ** -16) * spread[b, :m]
+            assert np.all(np.abs(got[b, :m] - ref[b, :m]) <= tol), b
+        # the commit, then the prune of what it left
+        want = {n: before[n].copy() for n in ("k", "v", "pos", "seq_len", "cur_pos")}
+        kd, vd = common.bf16_bits(d["kd"]), common.bf16_bits(d["vd"])
+        for b in range(B):
+            for j, node in enumerate(oracle.tree_path(d["parent"][b].tolist(), int(d["last"][b]))):
+                at = starts[b] + want["seq_len"][b]
+                want["k"][:, :, at], want["v"][:, :, at] = kd[:, :, b, node], vd[:, :, b, node]
+                want["pos"][:, :, at] = want["cur_pos"][b] + 1
+                want["seq_len"][b] += 1
+                want["cur_pos"][b] += 1
+        for n in want:
+            assert np.array_equal(joined[n], want[n]), n
+        ref = oracle.prune_window(_problem(a, want["k"], want["pos"], want["seq_len"], want["cur_pos"]),
+                                  want["v"], W)
+        _check_windowed(a, W, want, _state(a), sel.cpu().numpy(), ref)
+        pruned += int(np.sum(want["seq_len"] >= budget + W))
+    assert pruned == 2  # by the lengths alone
+
+
+def test_two_calls_at_once():
+    """Two streams with workspaces of their own: the CTAs of a call wait for one another, and
+    never for the other call's."""
+    a, b = Spec(lens=[5000, 700], N=16, seed=1), Spec(lens=[3000, 90, 2000], N=9, seed=2, block=16, Hq=4)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        a.attend(stream=streams[0])
+        b.attend(stream=streams[1])
+    torch.cuda.synchronize()
+    for s in (a, b):
+        assert tria.tria_get_device_error(s.ws) == 0
+        s.check()
+
+
+def test_largest_batch_and_shapes():
+    """256 sequences (some empty, some without nodes), and 256 nodes of 16 heads at D = 256."""
+    rng = np.random.default_rng(4)
+    s = Spec(lens=rng.integers(0, 200, 256).tolist(), N=4, nodes=rng.integers(0, 5, 256).tolist(),
+             Hq=2, Hkv=1, D=64, block=16)
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    s.check()
+    s = Spec(lens=[140], N=256, Hq=16, Hkv=1, D=256)
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    s.check()
+
+
+def test_a_cache_without_slots():
+    s = Spec(lens=[0, 0], slack=0, N=3)
+    assert s.cap == 0
+    s.t["k"] = torch.zeros(1, 2, 1, 128, dtype=torch.bfloat16, device="cuda")
+    s.cache = tria.Cache(s.t["k"], s.t["k"], torch.zeros(4, dtype=torch.int32, device="cuda"),
+                         s.t["seq_len"], s.t["cur_pos"], s.starts, cap_total=0)
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    s.check()
+
+
+def test_jumping_maxima():
+    """Logits that grow along the keys by less and by far more than the running maximum allows
+    without a change of scale, in both halves of a tile and between tiles; -0 and huge values."""
+    s = Spec(lens=[1500, 640], N=6, Hq=4, Hkv=2)
+    grow = torch.ones(1500)
+    grow[130:] = 8.0                       # inside a tile, in its second half
+    grow[400:] = 30.0
+    grow[900] = 600.0
+    for b, T in enumerate(s.lens):
+        at = torch.tensor(s._at(b, T))
+        s.k[:, :, at] = (s.k[:, :, at].float() * grow[:T].view(1, 1, T, 1)).to(torch.bfloat16)
+    s.t["k"].copy_(s.k)
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    s.check()
+
+
+def test_binding_refuses_strides_and_shapes():
+    s = Spec(lens=[20], N=3, Hq=4, Hkv=2, D=64)
+    with pytest.raises(ValueError, match="contiguous"):
+        tria.tria_tree_attention(s.cfg, s.cache, s.tree, 0, s.t["q"].transpose(1, 2).contiguous().transpose(1, 2),
+                                 s.t["out"], s.ws)
+    with pytest.raises(ValueError, match="q: expected"):
+        tria.tria_tree_attention(s.cfg, s.cache, s.tree, 0, s.t["q"][:, :2].contiguous(), s.t["out"], s.ws)
+    with pytest.raises(ValueError, match="out: expected"):
+        tria.tria_tree_attention(s.cfg, s.cache, s.tree, 0, s.t["q"], s.t["out"].float(), s.ws)
+    with pytest.raises(ValueError, match="last: expected"):
+        tria.tria_tree_commit(s.cfg, s.cache, s.tree, torch.zeros(2, dtype=torch.int32, device="cuda"), s.ws)
+    with pytest.raises(tria.TriaError, match="WORKSPACE"):
+        tria.tria_tree_attention(s.cfg, s.cache, s.tree, 0, s.t["q"], s.t["out"], s.ws[:1 << 20])

@@ -43,10 +43,10 @@ struct TreeCommitParams {
   int32_t *arrived;         // [B] blocks that are done with a sequence, zero at rest
   int32_t *err;
   int64_t cap;
-  int32_t L, Hkv, B, D, N, max_new;
+  int32_t L, Hkv, B, D, N, max_new, lg_per_block;
   int64_t seg_start[TRIA_MAX_BATCH + 1];
 };
-cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t s);
+cudaError_t launch_tree_commit(const TreeCommitParams &params, cudaStream_t s);
 
 struct alignas(64) TreeAttnParams {
   CUtensorMap tk, tv;       // K and V as [L*Hkv][cap][D], boxes of 64 columns x 128 rows (or a block)
@@ -73,7 +73,7 @@ struct alignas(64) TreeAttnParams {
 };
 // The tensor maps and what depends on the launch are filled in here; scratch holds
 // tree_attention_scratch bytes.
-cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t s);
+cudaError_t launch_tree_attention(const TreeAttnParams &params, cudaStream_t s);
 size_t tree_attention_scratch(int D, int G, int N);
 
 }  // namespace tria

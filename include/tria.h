@@ -178,7 +178,7 @@ typedef struct {
  * if that is -1.  A node count outside [0, max_nodes] sets TRIA_DEVERR_TREE and that
  * sequence is skipped; a parent outside [-1, i) sets it and counts as -1. */
 typedef struct {
-  const int32_t *parent;   /* DEVICE int32 [B][max_nodes]; entries past n_nodes[b] are not read */
+  const int32_t *parent;   /* DEVICE int32 [B][max_nodes]; entries past n_nodes[b] may hold anything */
   const int32_t *n_nodes;  /* DEVICE int32 [B] */
   const void *k;           /* DEVICE bf16 [L][Hkv][B][max_nodes][D], 16-byte aligned: the nodes' */
   const void *v;           /* post-RoPE keys and their values; rows past n_nodes[b] may hold anything */
@@ -315,8 +315,8 @@ tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *c
  * aligned; rows past n_nodes[b] are neither read nor written.  scale <= 0 selects
  * 1/sqrt(D).  What lies in slots past a sequence's length, in blocks that it does not hold
  * and in other branches of the tree does not reach a result, not even as a NaN.  Sums,
- * maxima and the output accumulate in float32; the weights are rounded to bf16 for their
- * product with V, and the output once to bf16.  A seq_len out of range sets
+ * maxima and the output accumulate in float32; the weights are rounded to bf16 (in their
+ * product with V and in their sum), and the output once to bf16.  A seq_len out of range sets
  * TRIA_DEVERR_SEQ_LEN and that sequence's rows are not written; a block id out of range
  * sets TRIA_DEVERR_PAGES and leaves that sequence's rows undefined.  ws of at least
  * tria_tree_workspace_size bytes; it must not overlap another call on the same workspace. */

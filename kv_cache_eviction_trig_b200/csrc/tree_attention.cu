@@ -14,12 +14,15 @@
 //                 a box per block of a paged cache), and the units' queries;
 //   warp 1        one thread issues the tensor products: S = Q K^T into tensor memory, and
 //                 O += P V with P read from tensor memory, where it overlays S;
-//   warps 4..     two warpgroups per M tile, a thread per row and half of the tile's keys: S
-//                 from tensor memory, the running maximum (the two threads of a row exchange
-//                 theirs) and sum, P = 2^(S - m) as bf16 back to tensor memory.
+//   warps 4..     two warpgroups of softmax: S from tensor memory, the running maximum and
+//                 sum, P = 2^(S - m) as bf16 back to tensor memory.  MT = 1: two threads per
+//                 row, each takes half of a tile's keys, and they exchange their maxima.
+//                 MT = 2: a thread per row of either M tile.
 // The next tile's S is computed while this one's softmax runs (MT = 1: two S buffers; MT = 2:
-// the M tiles alternate).  O stays in tensor memory and is rescaled only when a row's
-// maximum grew by more than 2^8 (P is at most 2^8 then; float32 sums lose nothing).
+// the M tiles alternate).  P is computed with the maximum so far; only if the tile's own is
+// larger by more than 2^8 is it computed again and O, which stays in tensor memory, rescaled
+// (P is at most 2^8 otherwise; float32 sums lose nothing).  A separate pass for the maximum
+// first took 0.5 of 2.6 thousand cycles per tile.
 // A unit that lies in one CTA is written from there.  The parts of the others go to the
 // workspace with their maxima and sums; once a CTA is through with its share it waits for the
 // other CTAs of its first and of its last unit and merges its share of their rows and columns,
@@ -38,7 +41,17 @@
 // so are Inf and NaN in the drafted V rows; the rows that do see such a node get them back
 // in the epilogue.
 //
-// What bounds it: K and V bytes for up to about 256 rows per KV head, the products above.
+// What bounds it (B200, 148 SMs).  Long keys with up to 128 rows per KV head: the K and V bytes;
+// 16 x 8192..32768 keys of 8 heads, D = 128, 16 to 32 nodes in pages of 64: 1.6 GB in 265 us,
+// 0.94 of the measured copy rate.  More rows: the chain product, softmax, product of an M tile
+// (4.2 thousand cycles per tile for the two M tiles, of which the tensor core works 2.0); a
+// chunk of up to 255 tokens with 8 heads per KV head: 580 TFLOP/s, 0.35 of the measured
+// matrix rate.  Short keys: latency; 2048 keys, 32 nodes: 14.6 us, of which 3 pass before the
+// first K tile arrives and 5 between the last tile and the last merged row.
+// Tried and slower: streams that split a tile's keys with an O of their own (288 us against
+// 269 on the long case above), softmax steps of 64 keys for two M tiles (61 us against 55 for
+// 32768 keys and 64 nodes: the products with N = 64 are not worth their reads of Q), four
+// warpgroups of softmax for two M tiles (78 us against 69: 96 registers per thread).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -50,10 +63,6 @@
 #include "mma_sync.cuh"
 #include "tcgen05.cuh"
 #include "tree.cuh"
-
-#ifndef TREE_NH2
-#define TREE_NH2 1
-#endif
 
 namespace tria {
 
@@ -77,7 +86,7 @@ struct TreeShape {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = QB * MT * TB;
   static constexpr int OFF_CTL = OFF_RING + NS * TB;
-  static constexpr int NH = MT == 2 ? TREE_NH2 : 2;      // threads per row
+  static constexpr int NH = MT == 2 ? 1 : 2;             // threads per row
   static constexpr int THREADS = 128 + 128 * NH * MT;
 };
 

@@ -200,8 +200,8 @@ class Config:
 
 def _want(t: torch.Tensor, dtype, shape, what: str):
     """A tensor's pointer, after a check that it is what the call reads or writes."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.dtype != dtype or t.shape != shape:  # (a tuple)
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     return _ptr(t)
 
 

@@ -132,8 +132,8 @@ typedef struct {
                            The prune window applies per unit: head budget + window. */
 } tria_config;
 
-/* A paged cache's bookkeeping (dimensionstp.github.io review, section 6, Limitations: in
- * serving, the pruned cache meets a paged KV cache).  The slots of a (layer, KV head) row
+/* A paged cache's bookkeeping (dimensionstp.github.io review, section 6, Limitations: serving
+ * with a paged KV cache).  The slots of a (layer, KV head) row
  * are n_blocks blocks of block_size; token t of sequence b lives in slot
  * block_table[b][t / block_size] * block_size + t % block_size, the same one in every row.
  * tria_block_tables keeps the arrays; a program fills them once: block_table all -1, held

@@ -42,16 +42,19 @@
 // in the epilogue.
 //
 // What bounds it (B200, 148 SMs).  Long keys with up to 128 rows per KV head: the K and V bytes;
-// 16 x 8192..32768 keys of 8 heads, D = 128, 16 to 32 nodes in pages of 64: 1.6 GB in 265 us,
-// 0.94 of the measured copy rate.  More rows: the chain product, softmax, product of an M tile
+// 16 x 8192..32768 keys of 8 heads, D = 128, 16 to 32 nodes in pages of 64: 1.6 GB in 268 us,
+// 0.93 of the measured copy rate (322 us back to back, where the SM clock falls and the softmax
+// warps' 2.4 thousand cycles per tile show).  More rows: the chain product, softmax, product of an M tile
 // (4.2 thousand cycles per tile for the two M tiles, of which the tensor core works 2.0); a
 // chunk of up to 255 tokens with 8 heads per KV head: 580 TFLOP/s, 0.35 of the measured
 // matrix rate.  Short keys: latency; 2048 keys, 32 nodes: 14.6 us, of which 3 pass before the
-// first K tile arrives and 5 between the last tile and the last merged row.
+// first K tile arrives and 6 between the last O and the last merged row.
 // Tried and slower: streams that split a tile's keys with an O of their own (288 us against
 // 269 on the long case above), softmax steps of 64 keys for two M tiles (61 us against 55 for
 // 32768 keys and 64 nodes: the products with N = 64 are not worth their reads of Q), four
-// warpgroups of softmax for two M tiles (78 us against 69: 96 registers per thread).
+// warpgroups of softmax for two M tiles (78 us against 69: 96 registers per thread), a quarter
+// of the exponentials by a polynomial on the FMA pipes (278 us against 268), P rounded there
+// (276).
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -748,6 +748,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
               if (!__any_sync(0xffffffffu, top > mr + 8.0f)) break;
               const float mn = mr == -INFINITY ? top : fmaxf(mr, mr + ceilf(top - mr));
               const float a = mr == -INFINITY ? 0.0f : exp2_approx(mr - mn);
+              tc::wait_st();  // O, or the first half of P, as the last change of scale left it
               if (kt > u.k0) {
                 outputs_before(x);
                 tc::fence_after();
@@ -763,7 +764,6 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
               }
               if (h > 0) {  // and the tile's first half of P
                 uint32_t o[32];
-                tc::wait_st();
                 tc::ld32(ts, o);
                 tc::wait_ld();
 #pragma unroll

@@ -1,0 +1,63 @@
+"""Tree attention over the forms where a CTA walks many key tiles: one and two M tiles, every
+head dimension, segments, pages and per-unit lengths, and logits that make the running maximum
+change.  The reference and the tolerances are those of test_gpu_tree.py."""
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_eviction_trig_b200 import tria
+from tests.test_gpu_tree import Spec, _lib  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+TILE = 128
+
+
+def _many_tiles(s, layer=0, per_cta=2):
+    """A CTA takes at least `per_cta` key tiles: the grid is at most the number of SMs."""
+    G = s.Hq // s.Hkv
+    m_tiles = 2 if s.D < 256 and s.N * G > TILE else 1
+    tiles = sum(-(-s.nodes[b] * G // (m_tiles * TILE)) *
+                (-(-s._len(layer, g, b) // TILE) - (-s.nodes[b] // TILE))
+                for b in range(s.B) for g in range(s.Hkv))
+    assert tiles > per_cta * torch.cuda.get_device_properties(0).multi_processor_count
+    return m_tiles
+
+
+def _run(s, layer=0, scale=None):
+    s.t["out"].fill_(7.0)
+    s.attend(layer, scale=scale)
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    s.check(layer, scale=scale)
+
+
+def _ladder(s, step):
+    """Keys whose logits climb in both halves of every tile: dimension 0 of the queries is 16,
+    that of the keys grows by `step` at the 10th and at the 74th key of a tile, and the other
+    dimensions add little."""
+    for b, T in enumerate(s.lens):
+        at = torch.tensor(s._at(b, T))
+        t = torch.arange(T)
+        level = step * (2 * (t // TILE) + (t % TILE >= 10).long() + (t % TILE >= 74).long()).float()
+        rows = 0.3 * s.k[:, :, at].float()
+        rows[..., 0] = level
+        s.k[:, :, at] = rows.to(torch.bfloat16)
+        s.q[b, :s.nodes[b], :, 0] = 16.0
+        top = step * 2.0 * (T // TILE + 1)
+        s.kd[:, :, b, :s.nodes[b], 0] = top
+    s.t["k"].copy_(s.k)
+    s.t["q"].copy_(s.q)
+    s.t["kd"].copy_(s.kd)
+
+
+# A step of 5 is 10.2 powers of two at D = 128 and 14.4 at D = 64 (the other dimensions move it
+# by at most about 2): past the 8 that a maximum may lag behind, in both halves of each tile.  What came before
+# then keeps a weight of 2^-10 or so per key, 60 keys of it: a change of scale that is lost
+# moves the result by several per cent, ten times the tolerance.
+@pytest.mark.parametrize("D,block", [(128, 0), (64, 0), (128, 32), (64, 256)])
+def test_two_m_tiles_rescaled_in_both_halves_of_a_tile(D, block):
+    s = Spec(D=D, Hq=32, Hkv=8, lens=[2400, 2100, 640], N=40, nodes=[40, 33, 36], block=block)
+    assert _many_tiles(s) == 2
+    _ladder(s, 5.0)
+    _run(s)

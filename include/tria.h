@@ -315,7 +315,8 @@ tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *c
  * aligned; rows past n_nodes[b] are neither read nor written.  scale <= 0 selects
  * 1/sqrt(D).  What lies in slots past a sequence's length, in blocks that it does not hold
  * and in other branches of the tree does not reach a result, not even as a NaN.  Sums,
- * maxima and the output accumulate in float32; the weights are rounded to bf16 (in their
+ * maxima and the output accumulate in float32, with a running maximum (no overflow for any
+ * finite products q . k); the weights are rounded to bf16 (in their
  * product with V and in their sum), and the output once to bf16.  A seq_len out of range sets
  * TRIA_DEVERR_SEQ_LEN and that sequence's rows are not written; a block id out of range
  * sets TRIA_DEVERR_PAGES and leaves that sequence's rows undefined.  ws of at least

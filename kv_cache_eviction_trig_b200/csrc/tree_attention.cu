@@ -15,7 +15,7 @@
 //   warp 1        one thread issues the tensor products: S = Q K^T into tensor memory, and
 //                 O += P V with P read from tensor memory, where it overlays S;
 //   warps 4..     two warpgroups of softmax: S from tensor memory, the running maximum and
-//                 sum, P = 2^(S - m) as bf16 back to tensor memory.  MT = 1: two threads per
+//                 sum, P = 2^((S - m) c) as bf16 back to tensor memory.  MT = 1: two threads per
 //                 row, each takes half of a tile's keys, and they exchange their maxima.
 //                 MT = 2: a thread per row of either M tile.
 // The next tile's S is computed while this one's softmax runs (MT = 1: two S buffers; MT = 2:
@@ -56,6 +56,7 @@
 // of the exponentials by a polynomial on the FMA pipes (278 us against 268), P rounded there
 // (276).
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -160,7 +161,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Two float32 products and sums at a time.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 // The tiles [k0, k1) of unit (b, g, mg), which has K tiles, KT of them cached.
@@ -244,6 +245,7 @@ template <int D, int ROWS, int DC, int AT>
 __device__ __forceinline__ void merge_items(const TreeAttnParams &p, const TreePart &t, int rank, int warps) {
   constexpr int PART = ROWS * (D + 2);
   const int lane = threadIdx.x & 31, parts = t.last - t.first + 1;
+  const float sl = p.scale * 1.4426950408889634f;
   const int rows = min((t.n - t.node0) * p.G, ROWS), groups = (rows + 31) / 32;
   for (int it = rank; it < groups * (D / DC); it += warps) {
     const int d0 = it / groups * DC, r = (it % groups) * 32 + lane;
@@ -267,8 +269,8 @@ __device__ __forceinline__ void merge_items(const TreeAttnParams &p, const TreeP
         if (i0 + i < parts) {
           // a part that saw nothing (its sum is 0) adds 0; a NaN in it stays one
           const float mc = v[i][DC], l1 = v[i][DC + 1], top = fmaxf(M, mc), ref = top == -INFINITY ? 0.0f : top;
-          const float a = exp2_approx(M - ref);  // (0 for the first part)
-          const float w = mc == -INFINITY ? (l1 == 0.0f ? 0.0f : 1.0f) : exp2_approx(mc - ref);
+          const float a = exp2_approx((M - ref) * sl);  // (0 for the first part)
+          const float w = mc == -INFINITY ? (l1 == 0.0f ? 0.0f : 1.0f) : exp2_approx((mc - ref) * sl);
           M = top;
           L = fmaf(L, a, w * l1);
 #pragma unroll
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     const int q4 = warp & 3, m = (warp - 4) / (4 * NH), half = NH == 2 ? ((warp - 4) >> 2) & 1 : 0;
     const int kid = tid - 128, row = q4 * 32 + lane, part_id = half * 128 + row;  // row of M tile m; its thread
     const uint32_t lane_off = (uint32_t)q4 << 21;              // 32 lanes of tensor memory
-    const float sl = p.scale * 1.4426950408889634f;            // logits in powers of two
+    const float sl = p.scale * 1.4426950408889634f;            // c: from S to powers of two
     const int per = kTile / p.G;                               // nodes per M tile
     const uint32_t pair = 2 + m * 4 + q4;                      // barrier of a row's two warps (NH = 2)
     Walk<MT> walk(p, c, X);
@@ -711,17 +713,19 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[i]);
             }
-            mr = sl * both(fmaxf(mx[0], mx[1]));
+            mr = both(fmaxf(mx[0], mx[1]));
           }
           // P with the maximum so far, which as a rule stands (within 2^8), 64 keys at a time;
-          // if theirs is larger, once more with that.  A maximum grows by whole powers of two,
-          // so that a change of scale is exact.
+          // if theirs is larger, once more with that.  A maximum grows by whole powers of two
+          // of P, so that a change of scale is exact up to the rounding of the maximum.
 #pragma unroll 1
           for (int h = 0; h < HK / 64; ++h) {
             float2 sum;
             uint32_t w[32];
             for (;;) {
               const float base = mr == -INFINITY ? 0.0f : mr;
+              // the difference first: scale * maximum may be so large that its rounding alone
+              // is a factor of many powers of two
               const float2 scale2 = make_float2(sl, sl), base2 = make_float2(-base, -base);
               float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
               float mx[2] = {-INFINITY, -INFINITY};
@@ -734,9 +738,9 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
                 if (e == 1) tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  const float2 y = fma2(make_float2(s[e][2 * i], s[e][2 * i + 1]), scale2, base2);
-                  mx[0] = fmaxf(mx[0], y.x);
-                  mx[1] = fmaxf(mx[1], y.y);
+                  const float2 y = mul2(add2(make_float2(s[e][2 * i], s[e][2 * i + 1]), base2), scale2);
+                  mx[0] = fmaxf(mx[0], s[e][2 * i]);
+                  mx[1] = fmaxf(mx[1], s[e][2 * i + 1]);
                   const float2 a = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                   const uint32_t r2 = pack_bf16x2(a.x, a.y);
                   sums[i & 1] = add2(sums[i & 1], make_float2(dev::bf16lo(r2), dev::bf16hi(r2)));
@@ -744,10 +748,14 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
                 }
               }
               sum = add2(sums[0], sums[1]);
-              const float top = base + both(fmaxf(mx[0], mx[1]));
-              if (!__any_sync(0xffffffffu, top > mr + 8.0f)) break;
-              const float mn = mr == -INFINITY ? top : fmaxf(mr, mr + ceilf(top - mr));
-              const float a = mr == -INFINITY ? 0.0f : exp2_approx(mr - mn);
+              const float top = both(fmaxf(mx[0], mx[1]));
+              const float rise = mr == -INFINITY ? (top == mr ? 0.0f : INFINITY) : (top - mr) * sl;
+              if (!__any_sync(0xffffffffu, rise > 8.0f)) break;
+              // (what it rises by past 2^128 leaves nothing of the terms before it)
+              const float mn = rise > 128.0f ? top
+                             : rise > 8.0f   ? fminf(fmaxf(top, mr + ceilf(rise) / sl), FLT_MAX)
+                                             : mr;
+              const float a = mn == mr ? 1.0f : exp2_approx((mr - mn) * sl);
               tc::wait_st();  // O, or the first half of P, as the last change of scale left it
               if (kt > u.k0) {
                 outputs_before(x);

@@ -5,7 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from kv_cache_eviction_trig_b200 import tria
+from tests import common
 from tests.test_gpu_tree import Spec, _lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,56 @@ def test_two_m_tiles_rescaled_in_both_halves_of_a_tile(D, block):
     assert _many_tiles(s) == 2
     _ladder(s, 5.0)
     _run(s)
+
+
+# Logits so large that they are one key's, or a few equal keys', in float32 and in float64 alike.
+# The queries have one dimension, so a logit before its scale is a product of two bf16 numbers
+# and exact in float32; two different ones of a row are more than 2^-8 of the largest apart,
+# millions of powers of two here.  What is left is the rounding of the weights and of the output.
+HUGE = {
+    "2^33": (17, 16, "mixed"),
+    "2^60": (30, 30, "mixed"),
+    "2^33 negative": (17, 16, "negative"),
+    "2^60 negative": (30, 30, "negative"),
+    "2^60 climbing": (30, 30, "climbing"),
+    "2^127 climbing": (64, 63, "climbing"),       # from -3e38 to 3e38: the difference is not finite
+}
+
+
+@pytest.mark.parametrize("D,N,block", [(64, 6, 0), (64, 70, 64), (128, 6, 32), (128, 70, 0), (256, 6, 0)])
+@pytest.mark.parametrize("name", sorted(HUGE))
+def test_huge_finite_logits(name, D, N, block):
+    qe, ke, kind = HUGE[name]
+    s = Spec(D=D, Hq=16, Hkv=4, lens=[700, 3, 2600], N=N, nodes=[N, N - 1, N - 3], block=block, seed=qe + D)
+    rng = np.random.default_rng(ke)
+
+    def bf16(x):  # of 8 bits, at most 1.98 in size
+        return np.clip(np.round(x * 64), -127, 127) / 64
+
+    for b, T in enumerate(s.lens):
+        n = s.nodes[b]
+        at = torch.tensor(s._at(b, T))
+        k = bf16(rng.uniform(-1.99, 1.99, (s.L, s.Hkv, T + n)))
+        q = bf16(rng.uniform(0.5, 1.99, (n, s.Hq)))
+        if kind == "climbing":
+            k = np.concatenate([np.sort(k[..., :T]), k[..., T:]], -1)
+            k[..., 0], k[..., T - 1], q[:] = -127 / 64, 127 / 64, 1.0
+        if kind == "negative":
+            k = -np.maximum(np.abs(k), 0.5)
+        k = torch.tensor(k * 2.0 ** ke, dtype=torch.float32).to(torch.bfloat16)
+        s.k[:, :, at, 0], s.kd[:, :, b, :n, 0] = k[..., :T], k[..., T:]
+        s.q[b, :n] = 0.0
+        s.q[b, :n, :, 0] = torch.tensor(q * 2.0 ** qe, dtype=torch.float32).to(torch.bfloat16)
+    for x in ("k", "kd", "q"):
+        s.t[x].copy_(getattr(s, x))
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    slots = [[s._at(b, s.lens[b])] * s.Hkv for b in range(s.B)]
+    ref, spread, _ = oracle.tree_attention(
+        common.bf16_bits(s.k), common.bf16_bits(s.v), slots, common.bf16_bits(s.kd),
+        common.bf16_bits(s.vd), s.parent, s.nodes, common.bf16_bits(s.q), 0, s.D ** -0.5)
+    got = s.t["out"].double().cpu().numpy()
+    for b, n in enumerate(s.nodes):
+        tol = 2.0 ** -7 * np.abs(ref[b, :n]) + (2.0 ** -8 + 2.0 ** -16) * spread[b, :n]
+        assert np.all(np.abs(got[b, :n] - ref[b, :n]) <= tol), b

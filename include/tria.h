@@ -316,8 +316,9 @@ tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *c
  * 1/sqrt(D).  What lies in slots past a sequence's length, in blocks that it does not hold
  * and in other branches of the tree does not reach a result, not even as a NaN.  Sums,
  * maxima and the output accumulate in float32, with a running maximum (no overflow for any
- * finite products q . k); the weights are rounded to bf16 (in their
- * product with V and in their sum), and the output once to bf16.  A seq_len out of range sets
+ * finite products q . k; a row whose logits are all -inf is NaN, as the formula is); the
+ * weights are rounded to bf16 (in their product with V and in their sum), and the output
+ * once to bf16.  A seq_len out of range sets
  * TRIA_DEVERR_SEQ_LEN and that sequence's rows are not written; a block id out of range
  * sets TRIA_DEVERR_PAGES and leaves that sequence's rows undefined.  ws of at least
  * tria_tree_workspace_size bytes; it must not overlap another call on the same workspace. */

@@ -278,7 +278,7 @@ __device__ __forceinline__ void merge_items(const TreeAttnParams &p, const TreeP
         }
       }
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const float inv = 1.0f / L;  // (0 only where all logits are -inf: such a row becomes NaN)
     uint2 *to = reinterpret_cast<uint2 *>(p.out + (((int64_t)t.b * p.N + t.node0 + r / p.G) * p.Hq + t.head0 + r % p.G) * D + d0);
 #pragma unroll
     for (int e = 0; e < DC; e += 4)
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       const bool whole = u.k0 == 0 && u.k1 == u.K;
       const int r = m * kTile + row;
       if (any) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = 1.0f / l;  // (l is 0 only where all logits are -inf: such a row becomes NaN)
         uint4 *to = reinterpret_cast<uint4 *>(p.out + (((int64_t)u.b * p.N + node) * p.Hq + head) * D);
         float *part = p.scratch + ((size_t)cta * kPartSlots + (u.k0 > 0 ? 0 : 1)) * (size_t)(MT * kTile) * (D + 2) + r;
         bool any_hurt = false;

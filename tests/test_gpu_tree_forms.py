@@ -116,3 +116,34 @@ def test_huge_finite_logits(name, D, N, block):
     for b, n in enumerate(s.nodes):
         tol = 2.0 ** -7 * np.abs(ref[b, :n]) + (2.0 ** -8 + 2.0 ** -16) * spread[b, :n]
         assert np.all(np.abs(got[b, :n] - ref[b, :n]) <= tol), b
+
+
+@pytest.mark.parametrize("D,N,lens", [(64, 6, [300, 0, 20000]), (128, 6, [300, 0, 9000]), (256, 6, [300, 0, 9000]),
+                                      (64, 70, [300, 0, 9000]), (128, 70, [300, 0, 20000])])
+def test_logits_of_minus_infinity(D, N, lens):
+    """A key of -inf has no weight beside a finite one; where a row sees nothing else, the softmax
+    is 0 / 0.  Sequence by sequence: all cached keys are -inf, node 1 is finite (its
+    descendants are its own); no cached key, node 1 is finite; all cached keys are -inf but the last."""
+    s = Spec(D=D, Hq=8, Hkv=2, lens=lens, N=N)
+    s.q[..., 1:] = 0.0
+    s.q[..., 0] = s.q[..., 0].float().abs().to(torch.bfloat16) + 0.5
+    for b, T in enumerate(lens):
+        at = torch.tensor(s._at(b, T), dtype=torch.long)
+        s.k[:, :, at, 0] = float("-inf")
+        s.kd[:, :, b, :, 0] = float("-inf")
+    s.kd[:, :, 0, 1, 0] = s.kd[:, :, 1, 1, 0] = 0.25
+    s.k[:, :, s.starts[2] + lens[2] - 1, 0] = -3.0
+    for x in ("k", "kd", "q"):
+        s.t[x].copy_(getattr(s, x))
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    got = s.t["out"].float().cpu()
+    for b in range(3):
+        for i in range(N):
+            path = oracle.tree_path(s.parent[b], i)
+            if b < 2 and 1 not in path:
+                assert torch.isnan(got[b, i]).all(), (b, i)
+                continue
+            seen = s.vd[0, :, b, 1] if b < 2 else s.v[0, :, s.starts[2] + lens[2] - 1]
+            assert torch.equal(got[b, i], seen.float().repeat_interleave(4, 0)), (b, i)

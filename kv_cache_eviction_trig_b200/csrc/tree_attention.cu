@@ -65,6 +65,7 @@
 #include <cudaTypedefs.h>
 
 #include "mma_sync.cuh"
+#include "ring.cuh"
 #include "tcgen05.cuh"
 #include "tree.cuh"
 
@@ -401,11 +402,13 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     Walk<MT> walk(p, c, X);
     Piece u;
     int x = 0, pi = 0;
+    int tiles = 0, queries = 0;  // copies issued: of K and V tiles (in the order of `seq`), of queries
     // a tile's K or V rows into ring place `seq`
     auto load = [&](const Piece &q, int kt, bool v, int seq, int32_t id) {
       const int s = seq % NS, use = seq / NS;
       if (use > 0) tree_wait(c, &c.empty[s], (use - 1) & 1, p.err);
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&c.abort))) return;
+      ++tiles;
       uint8_t *to = sm + S::OFF_RING + s * TB;
       const int lg = p.layer * p.Hkv + q.g;
       if (kt >= q.KT) {  // drafted nodes
@@ -457,6 +460,7 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       const int qb = pi % QB, quse = pi / QB;
       if (quse > 0) tree_wait(c, &c.q_empty[qb], (quse - 1) & 1, p.err);
       if (lane == 0 && !*reinterpret_cast<volatile int32_t *>(&c.abort)) {
+        ++queries;
         dev::mbar_arrive_expect_tx(&c.q_full[qb], (uint32_t)(MT * TB));
         for (int m = 0; m < MT; ++m)
           for (int cb = 0; cb < NB; ++cb)
@@ -481,10 +485,16 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
     }
     if (MT == 1) load(vu, vkt, true, v_seq<MT>(vx, X), vid);
     if (*reinterpret_cast<volatile int32_t *>(&c.abort)) {
-      // copies in flight land before the shared memory is given up
-      for (int i = 0; i < NS; ++i)
-        for (int k = 0; k < 2000 && !dev::mbar_try_wait(&c.full[i], 0) && !dev::mbar_try_wait(&c.full[i], 1); ++k) {
-        }
+      // copies in flight land before the shared memory is given up (lane 0 has issued the queries')
+      if (lane == 0) {
+        auto landed = [](uint64_t *bar, uint32_t parity) {
+          for (int k = 0; k < 2000 && !dev::mbar_try_wait(bar, parity); ++k) {
+          }
+        };
+        drain_ring(tiles, NS, [&](int i, uint32_t parity) { landed(&c.full[i], parity); });
+        drain_ring(queries, QB, [&](int i, uint32_t parity) { landed(&c.q_full[i], parity); });
+      }
+      __syncwarp();
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products

@@ -229,6 +229,12 @@ class Pages:
                    torch.arange(n_blocks, **i32), torch.tensor([0, n_blocks], **i32), block_size)
 
 
+# what a cache's tensors hold; the last word: exactly as many elements, or at least
+_CACHE_FIELDS = (("k", torch.bfloat16, False), ("v", torch.bfloat16, False),
+                 ("pos", torch.int32, False), ("seq_len", torch.int32, True),
+                 ("cur_pos", torch.int32, True), ("unit_len", torch.int32, True))
+
+
 class Cache:
     """tria_cache over torch tensors (k, v bf16 [L][Hkv][cap][D]; pos int32 [L][Hkv][cap];
     seq_len, cur_pos int32 [B] on the device; seq_start a host list of B+1 ints;
@@ -238,6 +244,8 @@ class Cache:
                  cap_total: Optional[int] = None, unit_len=None, pages: Optional[Pages] = None):
         self.tensors = (k, v, pos, seq_len, cur_pos, unit_len)
         self.pages = pages
+        self.held = [(t is not None, t is not None and t.numel(), t is not None and t.dtype)
+                     for t in self.tensors]
         self._starts = (ctypes.c_int64 * len(seq_start))(*seq_start)
         cap = cap_total if cap_total is not None else (k.shape[2] if k is not None else 0)
         self.c = tria_cache(_ptr(k), _ptr(v), _ptr(pos), _ptr(seq_len), _ptr(cur_pos),
@@ -372,6 +380,21 @@ def _check_device(t: torch.Tensor):
                          f"{torch.cuda.current_device()}")
 
 
+def _check_cache(cfg: Config, cache: Cache):
+    """The library sees pointers alone: the tensors have to hold what it reads and writes."""
+    c = cfg.c
+    B, units = c.batch, c.num_layers * c.n_kv_heads
+    if len(cache._starts) != B + 1:
+        raise ValueError(f"seq_start: expected {B + 1} entries, got {len(cache._starts)}")
+    rows = units * cache.c.cap_total
+    for (name, dtype, exact), want, (given, n, got) in zip(
+            _CACHE_FIELDS, (rows * c.head_dim, rows * c.head_dim, rows, B, B, units * B), cache.held):
+        if given and (got != dtype or (n != want if exact else n < want)):
+            raise ValueError(f"{name}: expected {dtype} of {want} elements, got {got} of {n}")
+    if cache.pages is not None and cache.pages.tensors[1].numel() != B:
+        raise ValueError(f"pages: expected tables of {B} sequences, got {cache.pages.tensors[1].numel()}")
+
+
 def _check_tree(cfg: Config, tree: Tree):
     c = cfg.c
     want = (c.num_layers, c.n_kv_heads, c.batch, tree.c.max_nodes, c.head_dim)
@@ -385,6 +408,7 @@ def tria_tree_attention(cfg: Config, cache: Cache, tree: Tree, layer: int, q: to
     """q, out: bf16 [B][N][Hq][D] device tensors; rows past a sequence's nodes are neither
     read nor written; scale None (or <= 0) lets the library use 1/sqrt(D)."""
     _check_tree(cfg, tree)
+    _check_cache(cfg, cache)
     _check_device(q)
     rows = (cfg.c.batch, tree.c.max_nodes, cfg.c.n_q_heads, cfg.c.head_dim)
     _check(lib().tria_tree_attention(
@@ -399,6 +423,7 @@ def tria_tree_commit(cfg: Config, cache: Cache, tree: Tree, last: torch.Tensor, 
     """last: int32 [B], each sequence's last accepted node or -1; slot_map: int32 [B][max_new]
     as tria_block_tables wrote it, for a paged cache."""
     _check_tree(cfg, tree)
+    _check_cache(cfg, cache)
     _check_device(last)
     B = cfg.c.batch
     max_new = 0 if slot_map is None else slot_map.shape[1]
@@ -413,6 +438,7 @@ def tria_block_tables(cfg: Config, cache: Cache, n_new: torch.Tensor,
                       slot_map: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
     """n_new: int32 [B], the tokens each sequence is about to add; slot_map: int32
     [B][max_new], or None to update the tables alone (n_new is then all 0)."""
+    _check_cache(cfg, cache)
     _check_device(n_new)
     B = cfg.c.batch
     max_new = 0 if slot_map is None else slot_map.shape[1]

@@ -198,6 +198,10 @@ class Config:
                    prune_window=prune_window, head_budgets=head_budgets)
 
 
+def _devices(tensors) -> set:
+    return {t.get_device() for t in tensors if t is not None}
+
+
 def _want(t: torch.Tensor, dtype, shape, what: str):
     """A tensor's pointer, after a check that it is what the call reads or writes."""
     if t.dtype != dtype or t.shape != shape:  # (a tuple)
@@ -213,6 +217,7 @@ class Pages:
                  ring_state: torch.Tensor, block_size: int):
         B, max_blocks = block_table.shape
         self.tensors = (block_table, held, ring, ring_state)
+        self.devices = _devices(self.tensors)
         self.block_size = block_size
         self.c = tria_pages(_want(block_table, torch.int32, (B, max_blocks), "block_table"),
                             _want(held, torch.int32, (B,), "held"),
@@ -244,6 +249,7 @@ class Cache:
                  cap_total: Optional[int] = None, unit_len=None, pages: Optional[Pages] = None):
         self.tensors = (k, v, pos, seq_len, cur_pos, unit_len)
         self.pages = pages
+        self.devices = _devices(self.tensors) | (pages.devices if pages else set())
         self.held = [(t is not None, t is not None and t.numel(), t is not None and t.dtype)
                      for t in self.tensors]
         self._starts = (ctypes.c_int64 * len(seq_start))(*seq_start)
@@ -267,6 +273,7 @@ class Tree:
         B, N = parent.shape
         L, Hkv, _, _, D = self.shape = tuple(k.shape)
         self.tensors = (parent, n_nodes, k, v)
+        self.devices = _devices(self.tensors)
         self.c = tria_tree(_want(parent, torch.int32, (B, N), "parent"),
                            _want(n_nodes, torch.int32, (B,), "n_nodes"),
                            _want(k, torch.bfloat16, (L, Hkv, B, N, D), "k"),
@@ -374,10 +381,15 @@ def tria_decode_attention(cfg: Config, cache: Cache, layer: int, q: torch.Tensor
                                        ws.numel(), _stream(stream)), "tria_decode_attention")
 
 
-def _check_device(t: torch.Tensor):
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on device {t.get_device()}, the current one is "
-                         f"{torch.cuda.current_device()}")
+def _check_device(*of):
+    """Tensors, caches and trees: all on the current device, where the library launches."""
+    current = torch.cuda.current_device()
+    for x in of:
+        if x is None:
+            continue
+        for d in (x.get_device(),) if isinstance(x, torch.Tensor) else x.devices:
+            if d != current:
+                raise ValueError(f"the tensors are on device {d}, the current one is {current}")
 
 
 def _check_cache(cfg: Config, cache: Cache):
@@ -409,7 +421,7 @@ def tria_tree_attention(cfg: Config, cache: Cache, tree: Tree, layer: int, q: to
     read nor written; scale None (or <= 0) lets the library use 1/sqrt(D)."""
     _check_tree(cfg, tree)
     _check_cache(cfg, cache)
-    _check_device(q)
+    _check_device(cache, tree, q, out, ws)
     rows = (cfg.c.batch, tree.c.max_nodes, cfg.c.n_q_heads, cfg.c.head_dim)
     _check(lib().tria_tree_attention(
         ctypes.byref(cfg.c), ctypes.byref(cache.c), ctypes.byref(tree.c), layer,
@@ -424,7 +436,7 @@ def tria_tree_commit(cfg: Config, cache: Cache, tree: Tree, last: torch.Tensor, 
     as tria_block_tables wrote it, for a paged cache."""
     _check_tree(cfg, tree)
     _check_cache(cfg, cache)
-    _check_device(last)
+    _check_device(cache, tree, last, slot_map, ws)
     B = cfg.c.batch
     max_new = 0 if slot_map is None else slot_map.shape[1]
     _check(lib().tria_tree_commit(
@@ -439,7 +451,7 @@ def tria_block_tables(cfg: Config, cache: Cache, n_new: torch.Tensor,
     """n_new: int32 [B], the tokens each sequence is about to add; slot_map: int32
     [B][max_new], or None to update the tables alone (n_new is then all 0)."""
     _check_cache(cfg, cache)
-    _check_device(n_new)
+    _check_device(cache, n_new, slot_map, ws)
     B = cfg.c.batch
     max_new = 0 if slot_map is None else slot_map.shape[1]
     _check(lib().tria_block_tables(

@@ -116,3 +116,49 @@ def test_a_configuration_of_another_batch(library):
 @pytest.mark.parametrize("pages", [False, True])
 def test_a_cache_smaller_than_the_configuration(library, pages, name, t):
     _refused(library, Calls(_cache(pages, **{name: t}, cap_total=CAP)), name + ": expected")
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another device."""
+
+    def get_device(self):
+        return 1
+
+
+def _elsewhere(t):
+    return t.as_subclass(Elsewhere)
+
+
+@pytest.mark.parametrize("name", ["k", "v", "pos", "seq_len", "cur_pos", "pages"])
+def test_a_cache_on_another_device(library, name):
+    c = _cache(True)
+    if name == "pages":
+        t = list(c.pages.tensors)
+        for i in range(4):
+            there = tria.Pages(*t[:i], _elsewhere(t[i]), *t[i + 1:], BLOCK)
+            _refused(library, Calls(_cache(there)), "on device 1, the current one is -1")
+    else:
+        t = c.tensors[["k", "v", "pos", "seq_len", "cur_pos"].index(name)]
+        _refused(library, Calls(_cache(True, **{name: _elsewhere(t)})), "on device 1")
+
+
+def test_arguments_on_another_device(library):
+    cfg, cache, ws = _cfg(), _cache(True), torch.zeros(4096, dtype=torch.uint8)
+    t = [_i32(B, N), _i32(B), _bf(L, HKV, B, N, D), _bf(L, HKV, B, N, D)]
+    tree, rows, slots, last = tria.Tree(*t), _bf(B, N, HQ, D), _i32(B, N), _i32(B)
+    trees = [tria.Tree(*t[:i], _elsewhere(t[i]), *t[i + 1:]) for i in range(4)]
+    e = _elsewhere
+    for call in ([lambda x=x: tria.tria_tree_attention(cfg, cache, x, 0, rows, rows, ws) for x in trees] +
+                 [lambda x=x: tria.tria_tree_commit(cfg, cache, x, last, ws, slot_map=slots) for x in trees] +
+                 [lambda: tria.tria_tree_attention(cfg, cache, tree, 0, e(rows), rows, ws),
+                  lambda: tria.tria_tree_attention(cfg, cache, tree, 0, rows, e(rows), ws),
+                  lambda: tria.tria_tree_attention(cfg, cache, tree, 0, rows, rows, e(ws)),
+                  lambda: tria.tria_tree_commit(cfg, cache, tree, e(last), ws, slot_map=slots),
+                  lambda: tria.tria_tree_commit(cfg, cache, tree, last, ws, slot_map=e(slots)),
+                  lambda: tria.tria_tree_commit(cfg, cache, tree, last, e(ws), slot_map=slots),
+                  lambda: tria.tria_block_tables(cfg, cache, e(last), slots, ws),
+                  lambda: tria.tria_block_tables(cfg, cache, last, e(slots), ws),
+                  lambda: tria.tria_block_tables(cfg, cache, last, slots, e(ws))]):
+        with pytest.raises(ValueError, match="on device 1"):
+            call()
+    assert library.calls == 0

@@ -7,6 +7,7 @@ built, or no CUDA device is present, the calls raise; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -198,8 +199,15 @@ class Config:
                    prune_window=prune_window, head_budgets=head_budgets)
 
 
-def _devices(tensors) -> set:
-    return {t.get_device() for t in tensors if t is not None}
+class _Tensors:
+    """What holds tensors is on their device, like one of them."""
+
+    def _hold(self, *tensors):
+        devices = sorted({t.get_device() for t in tensors if t is not None})
+        self._device = devices[0] if len(devices) == 1 else devices
+
+    def get_device(self):
+        return self._device
 
 
 def _want(t: torch.Tensor, dtype, shape, what: str):
@@ -209,7 +217,7 @@ def _want(t: torch.Tensor, dtype, shape, what: str):
     return _ptr(t)
 
 
-class Pages:
+class Pages(_Tensors):
     """tria_pages over int32 device tensors: block_table [B][max_blocks], held [B], ring
     [n_blocks] and ring_state [2] (head, free); see include/tria.h for how they start."""
 
@@ -217,7 +225,7 @@ class Pages:
                  ring_state: torch.Tensor, block_size: int):
         B, max_blocks = block_table.shape
         self.tensors = (block_table, held, ring, ring_state)
-        self.devices = _devices(self.tensors)
+        self._hold(*self.tensors)
         self.block_size = block_size
         self.c = tria_pages(_want(block_table, torch.int32, (B, max_blocks), "block_table"),
                             _want(held, torch.int32, (B,), "held"),
@@ -234,13 +242,11 @@ class Pages:
                    torch.arange(n_blocks, **i32), torch.tensor([0, n_blocks], **i32), block_size)
 
 
-# what a cache's tensors hold; the last word: exactly as many elements, or at least
-_CACHE_FIELDS = (("k", torch.bfloat16, False), ("v", torch.bfloat16, False),
-                 ("pos", torch.int32, False), ("seq_len", torch.int32, True),
-                 ("cur_pos", torch.int32, True), ("unit_len", torch.int32, True))
+_CACHE_FIELDS = (("k", torch.bfloat16), ("v", torch.bfloat16), ("pos", torch.int32),
+                 ("seq_len", torch.int32), ("cur_pos", torch.int32), ("unit_len", torch.int32))
 
 
-class Cache:
+class Cache(_Tensors):
     """tria_cache over torch tensors (k, v bf16 [L][Hkv][cap][D]; pos int32 [L][Hkv][cap];
     seq_len, cur_pos int32 [B] on the device; seq_start a host list of B+1 ints;
     optionally unit_len int32 [L][Hkv][B], the per-unit live lengths, or pages)."""
@@ -249,14 +255,22 @@ class Cache:
                  cap_total: Optional[int] = None, unit_len=None, pages: Optional[Pages] = None):
         self.tensors = (k, v, pos, seq_len, cur_pos, unit_len)
         self.pages = pages
-        self.devices = _devices(self.tensors) | (pages.devices if pages else set())
-        self.held = [(t is not None, t is not None and t.numel(), t is not None and t.dtype)
-                     for t in self.tensors]
+        self._hold(*self.tensors, *(pages.tensors if pages else ()))
         self._starts = (ctypes.c_int64 * len(seq_start))(*seq_start)
         cap = cap_total if cap_total is not None else (k.shape[2] if k is not None else 0)
         self.c = tria_cache(_ptr(k), _ptr(v), _ptr(pos), _ptr(seq_len), _ptr(cur_pos),
                             ctypes.cast(self._starts, ctypes.POINTER(ctypes.c_int64)), cap,
                             _ptr(unit_len), ctypes.pointer(pages.c) if pages else None)
+        # for the calls' checks: what the rows have room for, the sequences that the rest is for
+        n = [None if t is None else t.numel() if t.dtype == dtype else -1
+             for t, (_, dtype) in zip(self.tensors, _CACHE_FIELDS)]
+        self.room = min([x for x in n[:2] if x is not None], default=math.inf)
+        self.pos_room = math.inf if n[2] is None else n[2]
+        batches = {len(seq_start) - 1, *(x for x in n[3:5] if x is not None)}
+        if pages:
+            batches.add(pages.tensors[1].numel())
+        self.batch = batches.pop() if len(batches) == 1 else None
+        self.units = n[5]
 
     @classmethod
     def from_data(cls, data: dict) -> "Cache":
@@ -264,7 +278,7 @@ class Cache:
                    data["seq_start"])
 
 
-class Tree:
+class Tree(_Tensors):
     """tria_tree over device tensors: parent int32 [B][N], n_nodes int32 [B], and the drafted
     nodes' post-RoPE keys and values k, v bf16 [L][Hkv][B][N][D]."""
 
@@ -273,7 +287,7 @@ class Tree:
         B, N = parent.shape
         L, Hkv, _, _, D = self.shape = tuple(k.shape)
         self.tensors = (parent, n_nodes, k, v)
-        self.devices = _devices(self.tensors)
+        self._hold(*self.tensors)
         self.c = tria_tree(_want(parent, torch.int32, (B, N), "parent"),
                            _want(n_nodes, torch.int32, (B,), "n_nodes"),
                            _want(k, torch.bfloat16, (L, Hkv, B, N, D), "k"),
@@ -385,26 +399,26 @@ def _check_device(*of):
     """Tensors, caches and trees: all on the current device, where the library launches."""
     current = torch.cuda.current_device()
     for x in of:
-        if x is None:
-            continue
-        for d in (x.get_device(),) if isinstance(x, torch.Tensor) else x.devices:
-            if d != current:
-                raise ValueError(f"the tensors are on device {d}, the current one is {current}")
+        if x is not None and x.get_device() != current:
+            raise ValueError(f"the tensors are on device {x.get_device()}, the current one is {current}")
 
 
 def _check_cache(cfg: Config, cache: Cache):
     """The library sees pointers alone: the tensors have to hold what it reads and writes."""
     c = cfg.c
     B, units = c.batch, c.num_layers * c.n_kv_heads
+    rows = units * cache.c.cap_total
+    if (cache.batch == B and cache.room >= rows * c.head_dim and cache.pos_room >= rows
+            and cache.units in (None, units * B)):
+        return
     if len(cache._starts) != B + 1:
         raise ValueError(f"seq_start: expected {B + 1} entries, got {len(cache._starts)}")
-    rows = units * cache.c.cap_total
-    for (name, dtype, exact), want, (given, n, got) in zip(
-            _CACHE_FIELDS, (rows * c.head_dim, rows * c.head_dim, rows, B, B, units * B), cache.held):
-        if given and (got != dtype or (n != want if exact else n < want)):
-            raise ValueError(f"{name}: expected {dtype} of {want} elements, got {got} of {n}")
-    if cache.pages is not None and cache.pages.tensors[1].numel() != B:
-        raise ValueError(f"pages: expected tables of {B} sequences, got {cache.pages.tensors[1].numel()}")
+    want = (rows * c.head_dim, rows * c.head_dim, rows, B, B, units * B)
+    for (name, dtype), n, t in zip(_CACHE_FIELDS, want, cache.tensors):
+        short = t is not None and (t.numel() < n if name in ("k", "v", "pos") else t.numel() != n)
+        if t is not None and (short or t.dtype != dtype):
+            raise ValueError(f"{name}: expected {dtype} of {n} elements, got {t.dtype} of {t.numel()}")
+    raise ValueError(f"pages: expected tables of {B} sequences, got {cache.pages.tensors[1].numel()}")
 
 
 def _check_tree(cfg: Config, tree: Tree):

@@ -136,10 +136,10 @@ def test_a_cache_on_another_device(library, name):
         t = list(c.pages.tensors)
         for i in range(4):
             there = tria.Pages(*t[:i], _elsewhere(t[i]), *t[i + 1:], BLOCK)
-            _refused(library, Calls(_cache(there)), "on device 1, the current one is -1")
+            _refused(library, Calls(_cache(there)), "on device .*1.*, the current one is -1")
     else:
         t = c.tensors[["k", "v", "pos", "seq_len", "cur_pos"].index(name)]
-        _refused(library, Calls(_cache(True, **{name: _elsewhere(t)})), "on device 1")
+        _refused(library, Calls(_cache(True, **{name: _elsewhere(t)})), "on device .*1.*, the current")
 
 
 def test_arguments_on_another_device(library):
@@ -159,6 +159,6 @@ def test_arguments_on_another_device(library):
                   lambda: tria.tria_block_tables(cfg, cache, e(last), slots, ws),
                   lambda: tria.tria_block_tables(cfg, cache, last, e(slots), ws),
                   lambda: tria.tria_block_tables(cfg, cache, last, slots, e(ws))]):
-        with pytest.raises(ValueError, match="on device 1"):
+        with pytest.raises(ValueError, match="on device .*1.*, the current"):
             call()
     assert library.calls == 0

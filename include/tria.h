@@ -193,7 +193,7 @@ typedef struct {
 } tria_stats;
 
 /* Bytes of workspace the calls below need for this problem (the largest over
- * all calls).  The workspace holds the intermediate results of the steps the
+ * all calls that take its cache; those with a tree have tria_tree_workspace_size).  The workspace holds the intermediate results of the steps the
  * problem statement lists (dimensionstp.github.io review, section 2-1, steps
  * 1-6: score every cached key, normalise per head, keep the top budget, evict
  * the rest): folded weights, per-head scores, their sums, selection lists and

@@ -482,7 +482,8 @@ tria_status tria_workspace_size(const tria_config *cfg, const tria_cache *cache,
   if (s != TRIA_OK) return s;
   if (!cache || cache->cap_total < 0) return TRIA_ERR_INVALID_ARG;
   if (!cache->seq_start) return TRIA_ERR_INVALID_ARG;
-  *bytes = ws_layout(*cfg, cache->seq_start, cache->cap_total).total;
+  // (a cache with pages: tria_block_tables alone, the others refuse it or go by their tree)
+  *bytes = cache->pages ? kWsPrefix : ws_layout(*cfg, cache->seq_start, cache->cap_total).total;
   return TRIA_OK;
 }
 

@@ -70,6 +70,11 @@ typedef enum {
   TRIA_ERR_DEVICE_FLAG = 5    /* returned by tria_get_device_error when a device bit is set */
 } tria_status;
 
+/* Version of this header.  The structs below are read whole: a program built against another
+ * version (tria_cache has had `pages` since 0.2) must not call the library, and can tell by
+ * tria_version(), which begins with "tria " TRIA_VERSION " ". */
+#define TRIA_VERSION "0.2"
+
 #define TRIA_ROPE_HALF_SPLIT 0   /* pair f = (v[f], v[f + D/2]) */
 #define TRIA_ROPE_INTERLEAVED 1  /* pair f = (v[2f], v[2f + 1]) */
 
@@ -429,7 +434,7 @@ tria_status tria_prune_noalloc(const tria_config *cfg, const tria_stats *stats,
 const char *tria_status_string(tria_status s);
 
 /* Version string of this implementation of the prune step (romaanj.github.io
- * review, "Method"). */
+ * review, "Method"): "tria ", the TRIA_VERSION it was built with, and the GPU. */
 const char *tria_version(void);
 
 #ifdef __cplusplus

@@ -897,6 +897,6 @@ const char *tria_status_string(tria_status s) {
   return "TRIA_UNKNOWN_STATUS";
 }
 
-const char *tria_version(void) { return "tria 0.1 (sm_100a)"; }
+const char *tria_version(void) { return "tria " TRIA_VERSION " (sm_100a)"; }
 
 }  // extern "C"

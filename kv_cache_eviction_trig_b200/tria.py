@@ -36,6 +36,7 @@ MAX_SEGMENT = 1 << 18
 MAX_NODES = 256
 PRUNE_MAX_STAGES = 8
 NOALLOC_SCRATCH_BYTES = 16 << 20
+VERSION = "0.2"
 
 DEVERR_SEQ_LEN = 1
 DEVERR_SELECTION = 2
@@ -141,6 +142,9 @@ def lib():
         L.tria_status_string.argtypes = [ctypes.c_int]
         L.tria_status_string.restype = ctypes.c_char_p
         L.tria_version.restype = ctypes.c_char_p
+        if not L.tria_version().startswith(b"tria " + VERSION.encode() + b" "):
+            raise RuntimeError(f"{LIB_PATH} is {L.tria_version().decode()}, the binding's structs "
+                               f"are those of {VERSION}: build it with __graft_entry__.build()")
         for name in EXPORTS:
             if name not in ("tria_prune_stage_name", "tria_status_string", "tria_version"):
                 getattr(L, name).restype = ctypes.c_int

@@ -360,7 +360,8 @@ tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,
  *     that need any;
  *   - slot_map, DEVICE int32 [B][max_new], receives the slots of tokens seq_len[b]..
  *     seq_len[b] + n_new[b] - 1, and -1 after them; a sequence that does not hold the
- *     blocks for all of them gets -1 throughout.
+ *     blocks for all of them gets -1 throughout, and tokens whose block id is out of range
+ *     (TRIA_DEVERR_PAGES) get -1.
  * A sequence whose length or n_new is out of range (TRIA_DEVERR_SEQ_LEN), whose sum passes
  * its capacity (TRIA_DEVERR_SEGMENT_FULL) or whose held count is out of range
  * (TRIA_DEVERR_PAGES) keeps its blocks and gets -1s.  A ring_state out of range, or one

@@ -56,7 +56,12 @@ __device__ __forceinline__ void map_row(const BlockTablesParams &p, int b, int32
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       const int32_t t = len + i + k;
-      slot[k] = served && i + k < n ? (row[t >> p.shift] << p.shift) + (t & ((1 << p.shift) - 1)) : -1;
+      slot[k] = -1;
+      if (served && i + k < n) {
+        const int32_t id = row[t >> p.shift];
+        if (id >= 0 && id < p.n_blocks) slot[k] = (id << p.shift) + (t & ((1 << p.shift) - 1));
+        else dev::set_error(p.err, TRIA_DEVERR_PAGES);
+      }
     }
     if (W == 4 && whole) {
       *reinterpret_cast<int4 *>(to + i) = make_int4(slot[0], slot[1], slot[2], slot[3]);

@@ -145,7 +145,8 @@ typedef struct {
  * all 0, ring = 0..n_blocks-1 in any order, ring_state = {0, n_blocks}. */
 typedef struct {
   int32_t *block_table;    /* DEVICE int32 [B][max_blocks]: block ids, -1 past held[b] */
-  int32_t *held;           /* DEVICE int32 [B]: blocks that each sequence holds */
+  int32_t *held;           /* DEVICE int32 [B]: blocks that each sequence holds, at most max_blocks
+                              and TRIA_MAX_SEGMENT / block_size */
   int32_t *ring;           /* DEVICE int32 [n_blocks]: the pool, a ring of free block ids */
   int32_t *ring_state;     /* DEVICE int32 [2]: the ring's head, and how many blocks are free */
   int32_t block_size;      /* 16, 32, 64, 128 or 256 */

@@ -44,6 +44,13 @@ __device__ __forceinline__ Ask ask_of(const BlockTablesParams &p, int b, int *ba
   return a;
 }
 
+// Blocks that a sequence can hold: its row's entries, and those of the largest segment (so the
+// sums over the sequences below stay within 32 bits, whatever the counts say).
+__device__ __forceinline__ int32_t most_held(const BlockTablesParams &p) {
+  return min(p.max_blocks, TRIA_MAX_SEGMENT >> p.shift);
+}
+static_assert((int64_t)TRIA_MAX_BATCH * (TRIA_MAX_SEGMENT >> 4) < INT32_MAX, "sums of block counts");
+
 // Slots of sequence b's next tokens: W of its row's entries at a time, first, first + step, ....
 template <int W>
 __device__ __forceinline__ void map_row(const BlockTablesParams &p, int b, int32_t len, int32_t n,
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(kTableThreads)
   if (tid < p.B) {
     a = ask_of(p, tid, &bad);
     old = p.held[tid];
-    if (old < 0 || old > p.max_blocks) {
+    if (old < 0 || old > most_held(p)) {
       bad |= TRIA_DEVERR_PAGES;
       a.ok = false;
     }
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const __grid_cons
   int bad;
   const Ask a = ask_of(p, b, &bad);
   const int32_t held = p.held[b];
-  const bool served = a.ok && held >= 0 && held <= p.max_blocks &&
+  const bool served = a.ok && held >= 0 && held <= most_held(p) &&
                       (int64_t)a.len + a.n <= ((int64_t)held << p.shift);
   map_row<4>(p, b, a.len, a.n, served, blockIdx.x * kMapThreads + threadIdx.x, gridDim.x * kMapThreads);
 }

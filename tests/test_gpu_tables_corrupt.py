@@ -40,3 +40,19 @@ def test_bad_block_ids_name_no_slot(bad, max_new):
     assert slots[0, :20].tolist() == [14, 15] + [-1] * 16 + [32, 33]
     assert slots[1, :4].tolist() == [68, 69, 70, -1] and np.all(slots[:, 20:] == -1)
     assert pages.tensors[0].tolist() == table and pages.tensors[3].tolist() == [0, 2]
+
+
+def test_more_blocks_than_a_sequence_can_have():
+    """Counts within the rows of a wide table, but past any segment's blocks: the sequence keeps
+    what it has and gets no slots, the others are served.  (Sums of such counts over 256
+    sequences would pass 32 bits.)"""
+    most = tria.MAX_SEGMENT // 16
+    table = np.full((3, most + 8), -1)
+    table[1, 0], table[2, :most] = 7, 50 + np.arange(most)
+    ring = np.full(40000, -1)
+    ring[:20000] = 20000 + np.arange(20000)
+    pages, slots, code = _call(table, [most + 1, 1, most], ring, [0, 20000], 16, [3, 15, 0], [1, 2, 1], 2, 64)
+    assert code == tria.DEVERR_PAGES
+    assert slots.tolist() == [[-1, -1], [127, 16 * 20000], [50 * 16, -1]]
+    assert pages.tensors[1].tolist() == [most + 1, 2, 1]
+    assert pages.tensors[3].tolist() == [1, 20000 + most - 1 - 1]

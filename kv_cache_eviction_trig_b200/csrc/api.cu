@@ -734,6 +734,7 @@ tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,
   if (cache->pages ? (!slot_map || !aligned(slot_map, 4) || max_new < 1) : (slot_map || max_new))
     return TRIA_ERR_INVALID_ARG;
   if (cfg->head_dim > 256) return TRIA_ERR_UNSUPPORTED;
+  if ((int64_t)cfg->num_layers * cfg->n_kv_heads > INT32_MAX) return TRIA_ERR_UNSUPPORTED;
   if ((s = check_tree_ws(cfg, tree, ws, ws_bytes)) != TRIA_OK) return s;
   TreeCommitParams cp;
   std::memset(&cp, 0, sizeof cp);

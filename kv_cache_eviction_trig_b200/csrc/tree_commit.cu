@@ -132,8 +132,9 @@ cudaError_t launch_tree_commit(const TreeCommitParams &params, cudaStream_t s) {
   while ((int64_t)p.B * (((int64_t)p.L * p.Hkv + p.lg_per_block - 1) / p.lg_per_block) > 8ll * device_sm_count() &&
          p.lg_per_block < 64)
     p.lg_per_block *= 2;
+  // (a grid is at most 65535 blocks high; rows < 2^31)
+  while (((int64_t)p.L * p.Hkv + p.lg_per_block - 1) / p.lg_per_block > 65535) p.lg_per_block *= 2;
   const int64_t chunks = ((int64_t)p.L * p.Hkv + p.lg_per_block - 1) / p.lg_per_block;
-  if (chunks > 65535) return cudaErrorInvalidValue;
   tree_commit_kernel<<<dim3((unsigned)p.B, (unsigned)chunks), kCommitThreads, 0, s>>>(p);
   return cudaGetLastError();
 }

@@ -65,6 +65,74 @@ def test_two_m_tiles_rescaled_in_both_halves_of_a_tile(D, block):
     _run(s)
 
 
+# Each kernel (head dimension, M tiles) over many key tiles per CTA: rings that go round, both phases of every
+# barrier, changes of unit in the middle of a share, parts over several CTAs; keys that climb slowly
+# (the maximum lags behind them, within 2^8) or fast, and zeros of both signs.
+KERNELS = {"d64": dict(D=64, N=7), "d64 two M tiles": dict(D=64, N=13), "d128": dict(D=128, N=7),
+           "d128 two M tiles": dict(D=128, N=13), "d256": dict(D=256, N=7), "d256 more rows": dict(D=256, N=11)}
+
+
+@pytest.mark.parametrize("layout", ["segments", "pages of 16", "pages of 256", "unit lengths"])
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_many_tiles_per_cta(name, layout):
+    kw = dict(Hq=128, Hkv=8, nodes=[KERNELS[name]["N"], 5, KERNELS[name]["N"] - 1], **KERNELS[name])
+    if layout == "segments":
+        s = Spec(lens=[8100, 7000, 9300], **kw)
+    elif layout == "unit lengths":
+        lens = np.random.default_rng(3).integers(1000, 5000, (1, 8, 3))
+        lens[0, 2, 1], lens[0, 5, 0], lens[0, 7, 2] = 0, 1, 128
+        s = Spec(lens=[0, 0, 0], unit_lens=lens, **kw)
+        s.lens = [int(lens[0, :, b].max()) for b in range(3)]        # for the keys below
+    else:
+        s = Spec(lens=[4100, 1, 5333], block=int(layout.split()[-1]), **kw)
+    assert _many_tiles(s, per_cta=10 if layout == "segments" else 3) == (2 if "two" in name else 1)
+    _ladder(s, 5.0 if layout in ("segments", "pages of 256") else 0.7)
+    for x in ("k", "v", "kd", "vd", "q"):
+        zero = getattr(s, x)[..., 1::7]
+        zero[:] = torch.where(torch.isnan(zero), zero, torch.where(zero < 0, -0.0, 0.0).to(zero.dtype))
+        s.t[x].copy_(getattr(s, x))
+    _run(s)
+
+
+@pytest.mark.parametrize("block", [0, 64])
+@pytest.mark.parametrize("shape", ["tree", "chain"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_large_trees(D, shape, block):
+    """Tiles of nodes in the middle of a CTA's share, two of them per tree, with infinities and
+    NaN in values of some nodes of either tile: they reach those nodes' descendants, and no
+    other row."""
+    rng = np.random.default_rng(D + block)
+    s = Spec(D=D, Hq=8, Hkv=8, lens=rng.integers(0, 300, 24).tolist(), N=200, shape=shape, block=block,
+             nodes=rng.integers(0, 201, 24).tolist(), seed=block)
+    assert _many_tiles(s) == (1 if D == 256 else 2)
+    for b in range(0, 24, 2):
+        for node in rng.integers(0, 200, 3):
+            if node < s.nodes[b]:
+                s.vd[0, rng.integers(8), b, node, rng.integers(D)] = float("inf")
+                s.vd[0, rng.integers(8), b, node, rng.integers(D)] = float("nan")
+    s.t["vd"].copy_(s.vd)
+    s.t["out"].fill_(7.0)
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == 0
+    slots = [[s._at(b, s.lens[b])] * s.Hkv for b in range(s.B)]
+    ref, spread, steep = oracle.tree_attention(
+        common.bf16_bits(s.k), common.bf16_bits(s.v), slots, common.bf16_bits(s.kd),
+        common.bf16_bits(s.vd), s.parent, s.nodes, common.bf16_bits(s.q), 0, D ** -0.5)
+    got = s.t["out"].double().cpu().numpy()
+    poisoned = 0
+    for b, n in enumerate(s.nodes):
+        g, r = got[b, :n], ref[b, :n]
+        assert np.all(got[b, n:] == 7.0)
+        fine = np.isfinite(r)
+        poisoned += np.sum(~fine)
+        assert np.array_equal(np.isnan(g), np.isnan(r)) and np.array_equal(g[np.isinf(r)], r[np.isinf(r)]), b
+        tol = (2.0 ** -7 * np.abs(r) + (2.0 ** -8 + 2 * D * 2.0 ** -23 * steep[b, :n, :, None] + 2.0 ** -16) *
+               spread[b, :n])
+        assert np.all(np.abs(g[fine] - r[fine]) <= tol[fine]), b
+    assert poisoned > 0                      # (of the reference: some node was poisoned)
+
+
 # Logits so large that they are one key's, or a few equal keys', in float32 and in float64 alike.
 # The queries have one dimension, so a logit before its scale is a product of two bf16 numbers
 # and exact in float32; two different ones of a row are more than 2^-8 of the largest apart,

@@ -324,8 +324,8 @@ tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *c
  * maxima and the output accumulate in float32, with a running maximum (no overflow for any
  * finite products q . k; a row whose logits are all -inf is NaN, as the formula is); the
  * weights are rounded to bf16 (in their product with V and in their sum), and the output
- * once to bf16.  A seq_len out of range sets
- * TRIA_DEVERR_SEQ_LEN and that sequence's rows are not written; a block id out of range
+ * once to bf16.  A seq_len out of range sets TRIA_DEVERR_SEQ_LEN and that sequence's rows are
+ * not written (of a unit's length, the rows of its heads); a block id out of range
  * sets TRIA_DEVERR_PAGES and leaves that sequence's rows undefined.  ws of at least
  * tria_tree_workspace_size bytes; it must not overlap another call on the same workspace. */
 tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,

@@ -215,3 +215,27 @@ def test_logits_of_minus_infinity(D, N, lens):
                 continue
             seen = s.vd[0, :, b, 1] if b < 2 else s.v[0, :, s.starts[2] + lens[2] - 1]
             assert torch.equal(got[b, i], seen.float().repeat_interleave(4, 0)), (b, i)
+
+
+def test_a_bad_unit_length_skips_that_unit():
+    """Per-unit lengths: the heads of the other units are served; later units and sequences too."""
+    lens = np.array([[[300, 700, 64], [129, 900, 1000], [200, 40, 300]]])
+    s = Spec(Hq=12, Hkv=3, lens=[0, 0, 0], unit_lens=lens, N=9)
+    _run(s)
+    good = s.t["out"].clone()
+    s.t["unit_len"][0, 1, 0], s.t["unit_len"][0, 2, 1], s.t["unit_len"][0, 0, 2] = -1, 10 ** 6, 1041
+    s.t["out"].fill_(7.0)
+    s.attend()
+    torch.cuda.synchronize()
+    assert tria.tria_get_device_error(s.ws) == tria.DEVERR_SEQ_LEN
+    for b, g in ((0, 1), (1, 2), (2, 0)):
+        heads = slice(4 * g, 4 * g + 4)
+        assert torch.all(s.t["out"][b, :, heads] == 7.0)
+        s.t["out"][b, :, heads] = good[b, :, heads]
+    s.check()
+
+
+@pytest.mark.parametrize("D,N", [(64, 4), (128, 200)])
+def test_no_nodes_at_all(D, N):
+    s = Spec(D=D, lens=[300, 0], N=N, nodes=[0, 0])
+    _run(s)

@@ -173,7 +173,7 @@ tria_status check_cache(const tria_config *cfg, const tria_cache *c, bool need_k
   return TRIA_OK;
 }
 
-tria_status check_tree(const tria_config *cfg, const tria_tree *t, bool need_kv) {
+tria_status check_tree(const tria_tree *t, bool need_kv) {
   if (!t) return TRIA_ERR_INVALID_ARG;
   if (t->max_nodes < 1) return TRIA_ERR_INVALID_ARG;
   if (t->max_nodes > TRIA_MAX_NODES) return TRIA_ERR_UNSUPPORTED;
@@ -181,7 +181,6 @@ tria_status check_tree(const tria_config *cfg, const tria_tree *t, bool need_kv)
   if (!t->parent || !t->n_nodes || !aligned(t->parent, 4) || !aligned(t->n_nodes, 4))
     return TRIA_ERR_INVALID_ARG;
   if (!t->k || !t->v || !aligned(t->k, 16) || !aligned(t->v, 16)) return TRIA_ERR_INVALID_ARG;
-  (void)cfg;
   return TRIA_OK;
 }
 
@@ -673,7 +672,7 @@ tria_status tria_tree_workspace_size(const tria_config *cfg, const tria_cache *c
   if (!bytes || !cache) return TRIA_ERR_INVALID_ARG;
   tria_status s = check_config(cfg, false);
   if (s != TRIA_OK) return s;
-  if ((s = check_tree(cfg, tree, false)) != TRIA_OK) return s;
+  if ((s = check_tree(tree, false)) != TRIA_OK) return s;
   *bytes = tree_workspace_bytes(cfg, tree);
   return TRIA_OK;
 }
@@ -684,7 +683,7 @@ tria_status tria_tree_attention(const tria_config *cfg, const tria_cache *cache,
   tria_status s;
   if ((s = check_config(cfg, false)) != TRIA_OK) return s;
   if ((s = check_cache(cfg, cache, true, true)) != TRIA_OK) return s;
-  if ((s = check_tree(cfg, tree, true)) != TRIA_OK) return s;
+  if ((s = check_tree(tree, true)) != TRIA_OK) return s;
   if (layer < 0 || layer >= cfg->num_layers) return TRIA_ERR_INVALID_ARG;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return TRIA_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return TRIA_ERR_INVALID_ARG;
@@ -729,7 +728,7 @@ tria_status tria_tree_commit(const tria_config *cfg, const tria_cache *cache,
   tria_status s;
   if ((s = check_config(cfg, false)) != TRIA_OK) return s;
   if ((s = check_cache(cfg, cache, true, true)) != TRIA_OK) return s;
-  if ((s = check_tree(cfg, tree, true)) != TRIA_OK) return s;
+  if ((s = check_tree(tree, true)) != TRIA_OK) return s;
   if (!cache->cur_pos || !last || !aligned(last, 4)) return TRIA_ERR_INVALID_ARG;
   if (cache->pages ? (!slot_map || !aligned(slot_map, 4) || max_new < 1) : (slot_map || max_new))
     return TRIA_ERR_INVALID_ARG;

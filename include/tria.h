@@ -22,8 +22,8 @@
  *
  * Around the prune it has the steps of a decode loop over the pruned cache: one
  * token at a time (tria_append, tria_decode_attention), or a tree of drafted
- * tokens at a time (tria_tree_attention, tria_tree_commit), with the cache in one
- * segment per sequence or in pages (tria_pages, tria_block_tables).
+ * tokens at a time (tria_tree_attention, tria_tree_commit).  These two also take a
+ * cache in pages (tria_pages, tria_block_tables), which no call prunes.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -199,11 +199,12 @@ typedef struct {
 } tria_stats;
 
 /* Bytes of workspace the calls below need for this problem (the largest over
- * all calls that take its cache; those with a tree have tria_tree_workspace_size).  The workspace holds the intermediate results of the steps the
- * problem statement lists (dimensionstp.github.io review, section 2-1, steps
- * 1-6: score every cached key, normalise per head, keep the top budget, evict
- * the rest): folded weights, per-head scores, their sums, selection lists and
- * the error word.  Only the shapes and cache->seq_start/cap_total are read. */
+ * all calls that take its cache; those with a tree have tria_tree_workspace_size).
+ * The workspace holds the intermediate results of the steps the problem statement
+ * lists (dimensionstp.github.io review, section 2-1, steps 1-6: score every cached
+ * key, normalise per head, keep the top budget, evict the rest): folded weights,
+ * per-head scores, their sums, selection lists and the error word.  Only the shapes,
+ * cache->seq_start/cap_total and whether the cache has pages are read. */
 tria_status tria_workspace_size(const tria_config *cfg, const tria_cache *cache, size_t *bytes);
 
 /* Prepares a workspace for the steps of the problem statement (dimensionstp.github.io

@@ -25,8 +25,10 @@ constexpr int kTableCluster = 8;
 // Table entries above which the cluster of eight is taken.  One CTA and eight, per call: 2304
 // entries 4.2 and 4.9 us, 4608 4.5 and 5.2, 9216 5.6 and 5.6, 18432 7.5 and 5.6.
 constexpr int64_t kTableWide = 8192;
-// Slots up to which the first grid maps them itself.  Itself and by a second grid, per call:
+// Slots up to which the first grid maps them itself.  Itself and by a second grid, on the device:
 // 1024 slots 4.3 and 5.1 us, 4096 5.9 and 5.9, 8192 5.5 to 6.4 and 5.3 to 6.1, 16384 7.7 and 6.3.
+// Back to back a second launch also costs the host 2 us: 4096 slots 7.4 and 9.5 us a call, 8192 7.6 and
+// 9.7, 16384 8.3 and 9.7.  So 8192, where the device's times are the same.
 constexpr int64_t kMapInline = 8192;
 
 struct Ask {

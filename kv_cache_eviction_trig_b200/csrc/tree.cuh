@@ -1,5 +1,5 @@
-// Speculative decoding over the pruned cache: attention of drafted trees, the commit of
-// their accepted paths, and the block tables of a paged cache.
+// Speculative decoding over the cache: attention of drafted trees, the commit of their accepted
+// paths, and the block tables of a paged cache (which the prune does not take).
 #pragma once
 
 #include "tria_internal.cuh"

@@ -21,8 +21,11 @@
 // The next tile's S is computed while this one's softmax runs (MT = 1: two S buffers; MT = 2:
 // the M tiles alternate).  P is computed with the maximum so far; only if the tile's own is
 // larger by more than 2^8 is it computed again and O, which stays in tensor memory, rescaled
-// (P is at most 2^8 otherwise; float32 sums lose nothing).  A separate pass for the maximum
-// first took 0.5 of 2.6 thousand cycles per tile.
+// (P is at most 2^8 otherwise; float32 sums lose nothing; rescaling only past such a bound is a
+// published technique).  A separate pass for the maximum first took 0.5 of 2.6 thousand cycles
+// per tile.  The maximum is one of S, and its difference to S is formed before the scale: rounded
+// after it, a maximum past 2^31 would be off by factors of 2^128 (the extra operation: 61.9 us
+// against 60.6 for 32768 keys and 64 nodes).
 // A unit that lies in one CTA is written from there.  The parts of the others go to the
 // workspace with their maxima and sums; once a CTA is through with its share it waits for the
 // other CTAs of its first and of its last unit and merges its share of their rows and columns,
@@ -42,13 +45,16 @@
 // in the epilogue.
 //
 // What bounds it (B200, 148 SMs).  Long keys with up to 128 rows per KV head: the K and V bytes;
-// 16 x 8192..32768 keys of 8 heads, D = 128, 16 to 32 nodes in pages of 64: 1.6 GB in 268 us,
-// 0.93 of the measured copy rate (322 us back to back, where the SM clock falls and the softmax
-// warps' 2.4 thousand cycles per tile show).  More rows: the chain product, softmax, product of an M tile
+// 4 x 131072 keys of 8 heads, D = 128, 16 nodes: 2.15 GB in 356 us, 0.93 of the measured copy
+// rate; 16 x 8192..32768 keys, 16 to 32 nodes in pages of 64: 1.48 GB in 280 us, 0.82 (back to
+// back the SM clock falls, the softmax warps' 2.4 thousand cycles per tile show: 415 to 435
+// us and 285 to 325).  More rows: the chain product, softmax, product of an M tile
 // (4.2 thousand cycles per tile for the two M tiles, of which the tensor core works 2.0); a
-// chunk of up to 255 tokens with 8 heads per KV head: 580 TFLOP/s, 0.35 of the measured
-// matrix rate.  Short keys: latency; 2048 keys, 32 nodes: 14.6 us, of which 3 pass before the
-// first K tile arrives and 6 between the last O and the last merged row.
+// chunk of up to 255 tokens over 4 x 8.2K keys with 8 heads per KV head: 256 GFLOP in 354 us, 0.43
+// of the measured matrix rate.  Short keys: latency; 2048 keys, 32 nodes: 13 us on the device, of which
+// 3 pass before the first K tile arrives and 6 between the last O and the last merged row.
+// D = 64 carries half the bytes and products of D = 128 per softmax step: 0.15 of the floor with 49 nodes
+// of 8 heads over 23 x 3.9K..7.8K keys (84 us), 0.37 with 11 nodes over 9 x 3.6K..10.8K (58).
 // Tried and slower: streams that split a tile's keys with an O of their own (288 us against
 // 269 on the long case above), softmax steps of 64 keys for two M tiles (61 us against 55 for
 // 32768 keys and 64 nodes: the products with N = 64 are not worth their reads of Q), four
@@ -937,6 +943,10 @@ __global__ void __launch_bounds__(TreeShape<D, MT>::THREADS, 1)
       dev::named_barrier(1, ALL);
       // its items (32 rows by some output dims) over the warps of the unit's CTAs
       const int rank = (cta - t.first) * (ALL / 32) + (kid >> 5);
+      // Few dims and many parts at a time, or many dims and few parts; both for all units, us against
+      // this rule's: 17 parts of 2048 keys 16.5, 19.1 against 16.5; 16 x 2.1K keys, units over
+      // one to three CTAs, 63.3, 57.8 against 55.5; 32 nodes over 32768 keys 47.6, 51.3 against 46.6;
+      // 4 x 32 nodes over 8192 keys, units over five or six CTAs, 68.5, 67.5 against 69.7.
       if (parts > 4) merge_items<D, ROWS, MT == 2 ? 8 : 4, MT == 2 ? 8 : 10>(p, t, rank, parts * (ALL / 32));
       else merge_items<D, ROWS, 16, 4>(p, t, rank, parts * (ALL / 32));
       // the last of the unit's CTAs to be done leaves the counter at zero
@@ -977,7 +987,12 @@ bool map_3d(CUtensorMap *map, const void *base, int D, int64_t y, int64_t z, int
 }
 
 // M tiles per unit: two as soon as one does not hold the tree's rows (K and V are then read
-// once for 256 rows), but for D = 256, whose accumulator fills tensor memory.
+// once for 256 rows), but for D = 256, whose accumulator fills tensor memory.  By the tree's
+// capacity, as the host does not know the nodes.  Two and one M tile per unit, us: 255 tokens
+// over 4 x 4K..9K keys, 8 heads per KV head, D = 128 311 and 316, D = 64 250 and 267; 64 x 200 nodes, one head
+// per KV head 199 and 217; 4 x 32 nodes of 8 heads over 100..300 keys 22.6 and 25.8; 64 nodes of 4 heads
+// over 2048 keys 21.2 and 25.8, over 32768 62.1 and 62.1.  One is faster where few units have long
+// keys: 4 x 32 nodes of 8 heads over 8192 keys 70.8 and 67.7, over 2048 44.2 and 34.6.
 int m_tiles(int D, int G, int N) { return D < 256 && N * G > kTile ? 2 : 1; }
 
 template <int D, int MT>
